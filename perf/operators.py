@@ -77,7 +77,7 @@ def draw(rng):
         k, H = rng.randint(1, min(E, 10)), _log(rng, 16, 8192)
         if rng.random() < 0.7:
             H = (H + 7) // 8 * 8  # model widths are even; the others are odd sizes
-        T = _log(rng, 1, max(1, min(16384, 75_000_000 // (k * H))))
+        T = _log(rng, 1, max(1, min(16384, 75_000_000 // ((k + 2) * H))))
         c = {"op": op, "T": T, "E": E, "k": k, "H": H, "dtype": rng.choice(["f32", "bf16", "f16"] if op == "unsort" else ["bf16", "bf16", "f16", "f32"]),
              "train": rng.random() < 0.5, "pad": rng.random() < 0.5}
         if c["dtype"] == "f32":

@@ -13,6 +13,8 @@ Hardware"):
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -28,6 +30,8 @@ OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA,
 F16, BF16, F32, NVFP4, NVFP4_B32, NVFP4_MMA, NVFP4_B32_MMA = 0, 1, 2, 3, 4, 5, 6
 OP_MATMUL, OP_CONV = 0, 1
 ALGO_AUTO, ALGO_SKINNY, ALGO_TILED = 0, 1, 2
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+ACT_NONE, ACT_SWIGLU = 0, 1
 
 EXPORTS = ("sp24_status_string", "sp24_abi_version", "sp24_sizes", "sp24_check_24",
            "sp24_prune_compress_24", "sp24_decompress_24", "sp24_quantize_nvfp4_workspace_size",
@@ -39,7 +43,9 @@ EXPORTS = ("sp24_status_string", "sp24_abi_version", "sp24_sizes", "sp24_check_2
            "sp24_nvfp4_group_tensor_scale", "sp24_gemm_select", "sp24_gemm_choice", "sp24_gemm_auto",
            "sp24_gemm_choice_reset", "sp24_moe_block_workspace_size", "sp24_moe_block",
            "sp24_interleave_rows", "sp24_check_48", "sp24_prune_compress_48", "sp24_decompress_48",
-           "sp24_quantize_nvfp4_block32", "sp24_gemm_sparse48")
+           "sp24_quantize_nvfp4_block32", "sp24_gemm_sparse48", "sp24_moe_route", "sp24_moe_route_backward",
+           "sp24_moe_sort_workspace_size", "sp24_moe_sort", "sp24_moe_unsort", "sp24_moe_unsort_backward",
+           "sp24_quantize_w4", "sp24_dequantize_w4", "sp24_gemv_w4", "sp24_gemv_w4_grouped")
 
 _lock = threading.Lock()
 _lib = None
@@ -61,6 +67,11 @@ class _SparseOperand(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("values", ctypes.c_void_p),
                 ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p),
                 ("meta", ctypes.c_void_p)]
+
+
+class _W4Operand(ctypes.Structure):
+    _fields_ = [("scale_dtype", ctypes.c_int32), ("group", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
 def lib() -> ctypes.CDLL:
@@ -127,6 +138,17 @@ def lib() -> ctypes.CDLL:
             L.sp24_prepare_sparse_size.argtypes = [I64, I64, P]
             L.sp24_prepare_sparse.argtypes = [P, I64, I64, P, P]
             L.sp24_sparse48_to_mma.argtypes = [P, P, P, I64, I64, P, P, P, P]
+            W4 = ctypes.POINTER(_W4Operand)
+            L.sp24_moe_route.argtypes = [P, I, I64, I64, I, I, I, P, P, P]
+            L.sp24_moe_route_backward.argtypes = [P, I, P, P, I64, I64, I, I, I, P, P]
+            L.sp24_moe_sort_workspace_size.argtypes = [I64, I, I64, P]
+            L.sp24_moe_sort.argtypes = [P, I, P, I64, I, I64, I64, P, P, P, P, P, P, I64, P]
+            L.sp24_moe_unsort.argtypes = [P, I, P, P, I64, I, I64, I64, P, I, P]
+            L.sp24_moe_unsort_backward.argtypes = [P, I, P, I, P, P, I64, I, I64, I64, P, P, P]
+            L.sp24_quantize_w4.argtypes = [P, I, I64, I64, I, I, P, P, P, P]
+            L.sp24_dequantize_w4.argtypes = [W4, I64, I64, I, P, P]
+            L.sp24_gemv_w4.argtypes = [P, I, W4, I64, I64, I64, I, P, I, P]
+            L.sp24_gemv_w4_grouped.argtypes = [P, I, W4, P, I64, I64, I64, I64, I, P, I, P]
             L.sp24_peak_mma.argtypes = [I, I, P, P]
             L.sp24_peak_ctas.argtypes = [I]
             L.sp24_peak_read.argtypes = [P, I64, P, P]
@@ -822,4 +844,304 @@ def moe_block(x: torch.Tensor, routing: torch.Tensor, router_w: torch.Tensor, w_
         dd = ctypes.byref(_operand(w_down))
     _call("sp24_moe_block", ctypes.byref(xo), _ptr(routing), _ptr(router_w), T, topk, gd, gs, dd, ds, E, H, F,
           _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+    return out
+
+
+# ---------------------------------------------------------------------------- routed feed-forward
+
+def _placed(impl):
+    """Runs `impl` on the device of its first tensor and on `stream` (default: that device's current
+    stream), with what it allocates belonging to that stream.  Arguments after `out` are by name."""
+    name = next(iter(inspect.signature(impl).parameters))
+
+    @functools.wraps(impl)
+    def call(*args, stream=None, **kw):
+        t = args[0] if args else kw.get(name)
+        t = t.codes if isinstance(t, W4Tensor) else t
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+        dev = t.device
+        if stream is None and dev.index == torch.cuda.current_device():
+            return impl(*args, **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return impl(*args, **kw)
+    return call
+
+
+def _raw_stream(dev: torch.device) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _arg(t, name: str, dev: torch.device, shape, *dtypes) -> int:
+    """The address of an argument that has to be contiguous, on `dev`, and of this shape and type."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _check(st: int, fn: str) -> None:
+    if st != OK:
+        raise SP24Error(st, fn)
+
+
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _dims(t: torch.Tensor, name: str, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, not {t.dim()}")
+    return t.shape
+
+
+class MoeSorted(NamedTuple):
+    """Tokens in the order of their experts (sp24_moe_sort) with the tables of that order."""
+    xs: Optional[torch.Tensor]  # [T * topk, H] or None
+    pos: torch.Tensor           # int32 [T, topk]: row of (token, slot), -1 for an empty slot
+    src: torch.Tensor           # int32 [T * topk]: token * topk + slot of a row, -1 behind the last
+    row_expert: torch.Tensor    # int32 [T * topk]: expert of a row, -1 behind the last
+    offsets: torch.Tensor       # int32 [E + 1]
+
+
+@_placed
+def moe_route(logits: torch.Tensor, topk: int, scoring: int = ROUTE_SOFTMAX, renormalize: bool = True, out=None):
+    """(routing int32 [T, topk], router_w fp32 [T, topk]) of router logits [T, E]: the topk largest
+    logits (ties to the lower expert) and their softmax or sigmoid weights."""
+    dev = logits.device
+    T, E = _dims(logits, "logits", 2)
+    lp = _arg(logits, "logits", dev, logits.shape, *_FLOATS)
+    if out is None:
+        out = (torch.empty((T, topk), dtype=torch.int32, device=dev),
+               torch.empty((T, topk), dtype=torch.float32, device=dev))
+    routing, w = out
+    _check(lib().sp24_moe_route(lp, _DT[logits.dtype], T, E, topk, scoring, bool(renormalize),
+                                _arg(routing, "routing", dev, (T, topk), torch.int32),
+                                _arg(w, "router_w", dev, (T, topk), torch.float32), _raw_stream(dev)), "sp24_moe_route")
+    return routing, w
+
+
+@_placed
+def moe_route_backward(d_router_w: torch.Tensor, logits: torch.Tensor, routing: torch.Tensor,
+                       scoring: int = ROUTE_SOFTMAX, renormalize: bool = True, out=None) -> torch.Tensor:
+    """The gradient of moe_route's logits (their type, [T, E]) from that of its weights."""
+    dev = logits.device
+    T, E = _dims(logits, "logits", 2)
+    topk = _dims(routing, "routing", 2)[1]
+    lp = _arg(logits, "logits", dev, logits.shape, *_FLOATS)
+    if out is None:
+        out = torch.empty_like(logits)
+    _check(lib().sp24_moe_route_backward(lp, _DT[logits.dtype], _arg(routing, "routing", dev, (T, topk), torch.int32),
+                                         _arg(d_router_w, "d_router_w", dev, (T, topk), torch.float32), T, E, topk,
+                                         scoring, bool(renormalize), _arg(out, "out", dev, (T, E), logits.dtype),
+                                         _raw_stream(dev)), "sp24_moe_route_backward")
+    return out
+
+
+def moe_sort_workspace_bytes(T: int, topk: int, E: int) -> int:
+    n = ctypes.c_int64(0)
+    _call("sp24_moe_sort_workspace_size", T, topk, E, ctypes.byref(n))
+    return n.value
+
+
+def _sort(x, routing, E: int, out, workspace) -> MoeSorted:
+    dev = routing.device
+    T, topk = _dims(routing, "routing", 2)
+    n = T * topk
+    xp = xsp = None
+    H, dt = 0, F32
+    if x is not None:
+        H, dt = _dims(x, "x", 2)[1], _dtype_code(x)
+        xp = _arg(x, "x", dev, (T, H), *_FLOATS)
+    if out is None:
+        i32 = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+        out = (None if x is None else torch.empty((n, H), dtype=x.dtype, device=dev), i32(T, topk), i32(n), i32(n), i32(E + 1))
+    xs, pos, src, row_expert, offsets = out
+    if x is not None:
+        xsp = _arg(xs, "xs", dev, (n, H), x.dtype)
+    ws = moe_sort_workspace_bytes(T, topk, E)
+    if workspace is None and ws:
+        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    wp, wn = (None, 0) if workspace is None else (_arg(workspace, "workspace", dev, workspace.shape, torch.uint8), workspace.numel())
+    _check(lib().sp24_moe_sort(xp, dt, _arg(routing, "routing", dev, (T, topk), torch.int32), T, topk, E, H, xsp,
+                               _arg(pos, "pos", dev, (T, topk), torch.int32), _arg(src, "src", dev, (n,), torch.int32),
+                               _arg(row_expert, "row_expert", dev, (n,), torch.int32),
+                               _arg(offsets, "offsets", dev, (E + 1,), torch.int32), wp, wn, _raw_stream(dev)),
+           "sp24_moe_sort")
+    return MoeSorted(xs, pos, src, row_expert, offsets)
+
+
+@_placed
+def moe_sort(x: torch.Tensor, routing: torch.Tensor, E: int, out=None, workspace=None) -> MoeSorted:
+    """x [T, H] in the order of the experts in routing [T, topk] (stable), with the tables of that
+    order.  An id of -1 is an empty slot; rows of xs behind the last expert's are not written."""
+    return _sort(x, routing, E, out, workspace)
+
+
+@_placed
+def moe_sort_tables(routing: torch.Tensor, E: int, out=None, workspace=None) -> MoeSorted:
+    """moe_sort without the rows: the tables only (xs is None)."""
+    return _sort(None, routing, E, out, workspace)
+
+
+def _unsort(ys, pos, router_w, dtype, out):
+    dev = ys.device
+    rows, H = _dims(ys, "ys", 2)
+    T, topk = _dims(pos, "pos", 2)
+    yp = _arg(ys, "ys", dev, ys.shape, *_FLOATS)
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype or ys.dtype, device=dev)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, not {out.dtype}")
+    wp = None if router_w is None else _arg(router_w, "router_w", dev, (T, topk), torch.float32)
+    _check(lib().sp24_moe_unsort(yp, _DT[ys.dtype], _arg(pos, "pos", dev, (T, topk), torch.int32), wp, T, topk, rows, H,
+                                 _arg(out, "out", dev, (T, H), *_FLOATS), _DT[out.dtype], _raw_stream(dev)),
+           "sp24_moe_unsort")
+    return out
+
+
+@_placed
+def moe_sort_backward(dxs: torch.Tensor, pos: torch.Tensor, out=None) -> torch.Tensor:
+    """The gradient of moe_sort's x from that of xs: each token's rows summed (fp32, slot order)."""
+    return _unsort(dxs, pos, None, dxs.dtype, out)
+
+
+@_placed
+def moe_unsort(ys: torch.Tensor, pos: torch.Tensor, router_w: Optional[torch.Tensor] = None, dtype=None,
+               out=None) -> torch.Tensor:
+    """y[t] = sum_s router_w[t, s] ys[pos[t, s]] (None: weights of 1), in ys's type or `dtype`."""
+    return _unsort(ys, pos, router_w, dtype, out)
+
+
+@_placed
+def moe_unsort_backward(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, router_w: Optional[torch.Tensor] = None,
+                        out=None):
+    """(dys, d_router_w) of moe_unsort; rows of dys that no slot names are not written (zeros when
+    allocated here).  Without router_w, d_router_w is None."""
+    dev = ys.device
+    rows, H = _dims(ys, "ys", 2)
+    T, topk = _dims(pos, "pos", 2)
+    yp = _arg(ys, "ys", dev, ys.shape, *_FLOATS)
+    if out is None:
+        out = (torch.zeros_like(ys), None if router_w is None else torch.empty((T, topk), dtype=torch.float32, device=dev))
+    dys, dw = out
+    wp = None if router_w is None else _arg(router_w, "router_w", dev, (T, topk), torch.float32)
+    dwp = None if dw is None else _arg(dw, "d_router_w", dev, (T, topk), torch.float32)
+    _check(lib().sp24_moe_unsort_backward(_arg(dy, "dy", dev, (T, H), *_FLOATS), _DT[dy.dtype], yp, _DT[ys.dtype],
+                                          _arg(pos, "pos", dev, (T, topk), torch.int32), wp, T, topk, rows, H,
+                                          _arg(dys, "dys", dev, (rows, H), ys.dtype), dwp, _raw_stream(dev)),
+           "sp24_moe_unsort_backward")
+    return dys, dw
+
+
+# ---------------------------------------------------------------------------- 4-bit group weights
+
+class W4Tensor(NamedTuple):
+    """4-bit weights with group scales: codes uint8 [rows, K/2] (entry 2i in the low nibble), scales
+    [rows, K/group] f16 / bf16, zeros uint8 [rows, K/group] or None (8): value = (q - z) * s."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: Optional[torch.Tensor] = None
+
+
+def _w4(w: W4Tensor, dev: torch.device):
+    """(C operand, rows, K) of 4-bit weights on `dev`."""
+    rows, half = _dims(w.codes, "codes", 2)
+    K = 2 * half
+    groups = _dims(w.scales, "scales", 2)[1]
+    group = K // groups if groups else 128
+    if groups * group != K:
+        raise ValueError(f"{groups} groups do not divide {K} entries")
+    op = _W4Operand(_DT.get(w.scales.dtype, -1), group, _arg(w.codes, "codes", dev, (rows, half), torch.uint8),
+                    _arg(w.scales, "scales", dev, (rows, groups), *_HALVES),
+                    None if w.zeros is None else _arg(w.zeros, "zeros", dev, (rows, groups), torch.uint8))
+    return op, rows, K
+
+
+@_placed
+def quantize_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, out: Optional[W4Tensor] = None) -> W4Tensor:
+    """4-bit codes of a 16-bit weight [rows, K], rounded to nearest, with one scale per `group`
+    entries (symmetric), or with a zero point beside each scale."""
+    dev = w.device
+    R, K = _dims(w, "w", 2)
+    wp = _arg(w, "w", dev, w.shape, *_HALVES)
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError(f"groups of 32, 64 or 128 that divide K = {K}, not {group}")
+    if out is None:
+        out = W4Tensor(torch.empty((R, K // 2), dtype=torch.uint8, device=dev),
+                       torch.empty((R, K // group), dtype=w.dtype, device=dev),
+                       torch.empty((R, K // group), dtype=torch.uint8, device=dev) if zeros else None)
+    zp = _arg(out.zeros, "zeros", dev, (R, K // group), torch.uint8) if zeros else None
+    _check(lib().sp24_quantize_w4(wp, _DT[w.dtype], R, K, group, bool(zeros),
+                                  _arg(out.codes, "codes", dev, (R, K // 2), torch.uint8),
+                                  _arg(out.scales, "scales", dev, (R, K // group), w.dtype), zp, _raw_stream(dev)),
+           "sp24_quantize_w4")
+    return out
+
+
+@_placed
+def dequantize_w4(w: W4Tensor, dtype=torch.float32, out=None) -> torch.Tensor:
+    """The values (q - z) * s of 4-bit weights, rounded once to `dtype`."""
+    dev = w.codes.device
+    op, rows, K = _w4(w, dev)
+    if out is None:
+        out = torch.empty((rows, K), dtype=dtype, device=dev)
+    _check(lib().sp24_dequantize_w4(ctypes.byref(op), rows, K, _DT[dtype], _arg(out, "out", dev, (rows, K), dtype),
+                                    _raw_stream(dev)), "sp24_dequantize_w4")
+    return out
+
+
+def _gemv_out(x, rows: int, N: int, act: int, dtype, out):
+    cols = N // 2 if act == ACT_SWIGLU else N
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype or (x.dtype if act == ACT_SWIGLU else torch.float32), device=x.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, not {out.dtype}")
+    return out, _arg(out, "out", x.device, (rows, cols), torch.float32, x.dtype)
+
+
+@_placed
+def gemv_w4(x: torch.Tensor, w: W4Tensor, act: int = ACT_NONE, dtype=None, out=None) -> torch.Tensor:
+    """y[M, N] = x[M, K] @ value(w)[N, K]^T for a few rows x (f16 / bf16), fp32 (or x's type by
+    `dtype`); ACT_SWIGLU: w holds gate rows then up rows, y[M, N/2] = SiLU(gate) * up in x's type."""
+    dev = x.device
+    M, K = _dims(x, "x", 2)
+    xp = _arg(x, "x", dev, x.shape, *_HALVES)
+    op, N, Kw = _w4(w, dev)
+    if K != Kw:
+        raise ValueError(f"K mismatch: {K} vs {Kw}")
+    out, yp = _gemv_out(x, M, N, act, dtype, out)
+    _check(lib().sp24_gemv_w4(xp, _DT[x.dtype], ctypes.byref(op), M, N, K, act, yp, _DT[out.dtype], _raw_stream(dev)),
+           "sp24_gemv_w4")
+    return out
+
+
+@_placed
+def gemv_w4_grouped(xs: torch.Tensor, w: W4Tensor, offsets: torch.Tensor, act: int = ACT_NONE, dtype=None,
+                    out=None) -> torch.Tensor:
+    """gemv_w4 over rows in expert order (moe_sort's xs and offsets [E + 1]) with the E matrices
+    stacked in w; rows from offsets[E] on are not written (zeros when allocated here)."""
+    dev = xs.device
+    R, K = _dims(xs, "xs", 2)
+    xp = _arg(xs, "xs", dev, xs.shape, *_HALVES)
+    op, rows, Kw = _w4(w, dev)
+    E = _dims(offsets, "offsets", 1)[0] - 1
+    if K != Kw:
+        raise ValueError(f"K mismatch: {K} vs {Kw}")
+    if E < 1 or rows % E:
+        raise ValueError(f"{rows} weight rows are not those of {E} experts")
+    N = rows // E
+    if out is None:
+        cols = N // 2 if act == ACT_SWIGLU else N
+        out = torch.zeros((R, cols), dtype=dtype or (xs.dtype if act == ACT_SWIGLU else torch.float32), device=dev)
+    out, yp = _gemv_out(xs, R, N, act, dtype, out)
+    _check(lib().sp24_gemv_w4_grouped(xp, _DT[xs.dtype], ctypes.byref(op), _arg(offsets, "offsets", dev, (E + 1,), torch.int32),
+                                      R, E, N, K, act, yp, _DT[out.dtype], _raw_stream(dev)), "sp24_gemv_w4_grouped")
     return out

@@ -506,6 +506,128 @@ int sp24_moe_block(const sp24_operand* x, const int32_t* routing, const float* r
 int sp24_interleave_rows(const void* a, const void* b, int64_t rows, int64_t row_bytes,
                          int64_t block_rows, void* out, void* stream);
 
+/* ----------------------------------------------------------------------- routed feed-forward */
+/* The steps around the experts' products ([P1] "Concurrency, not sparsity, is the lever": tokens
+ * routed top-k to E experts), with their gradients.  The formulas are not on the source pages.
+ * Deterministic: no result depends on the order of atomics.
+ *
+ * Router.  logits: device, F32/F16/BF16, [T, E].  Per token the topk largest logits, in descending
+ * order, equal ones by the lower index; NaN and -inf are never selected.  A slot that nothing is
+ * left for gets id -1 and weight 0 (a row of -inf: all of them).
+ *   SP24_ROUTE_SOFTMAX: w_s = exp(l_s) / sum exp(l), the sum over all experts, or over the selected
+ *                       ones when renormalize != 0.
+ *   SP24_ROUTE_SIGMOID: w_s = 1 / (1 + exp(-l_s)), divided by the selected ones' sum when
+ *                       renormalize != 0 (0 when that sum is 0).
+ *   Computed in fp32 (softmax about the row's maximum).  A selected +inf, or a NaN among the
+ *   logits a softmax sums over, gives the row NaN weights as the formula does.
+ *   routing: device int32 [T, topk]; router_w: device fp32 [T, topk].
+ * sp24_moe_route_backward: dlogits (device, logits' type, [T, E], written whole) from d_router_w
+ *   (device fp32 [T, topk]), with the weights recomputed from logits and routing; the selection is
+ *   constant.  Ids outside [0, E) are empty slots (their d_router_w is not read into anything), ids
+ *   other than -1 among them set the device error word (SP24_ERR_INVALID_ARG); an id met twice
+ *   collects both slots.  Where nothing was selected dlogits is 0; a -inf logit gets 0.
+ * 1 <= E <= 1024 and 1 <= topk <= min(E, 32) (SP24_ERR_UNSUPPORTED above, SP24_ERR_SHAPE for sizes
+ * that make no sense); T up to 2^31 - 1.  T == 0 is a no-op.  One launch each, no workspace. */
+enum { SP24_ROUTE_SOFTMAX = 0, SP24_ROUTE_SIGMOID = 1 };
+int sp24_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int topk, int scoring,
+                   int renormalize, int32_t* routing, float* router_w, void* stream);
+int sp24_moe_route_backward(const void* logits, int dtype, const int32_t* routing, const float* d_router_w,
+                            int64_t T, int64_t E, int topk, int scoring, int renormalize, void* dlogits,
+                            void* stream);
+
+/* Token sort: the n = T topk (token, slot) entries in the order of their experts, entries of one
+ * expert in their own order (a stable sort).  For row r of that order and entry i = t topk + s:
+ *   offsets     device int32 [E + 1]: expert e's rows are offsets[e] .. offsets[e + 1] - 1
+ *   pos         device int32 [T, topk]: the row of entry i, -1 for an empty slot (id -1)
+ *   src         device int32 [n]: the entry of row r, -1 for r >= offsets[E]
+ *   row_expert  device int32 [n]: the expert of row r, -1 for r >= offsets[E] (with topk = 1 the
+ *               routing of sp24_gemm_grouped over xs when no slot is empty)
+ *   xs          device [n, H], x's type: xs[r] = x[src[r] / topk]; rows r >= offsets[E] are left as
+ *               they were.
+ * x (device, F32/F16/BF16, [T, H]) and xs may both be NULL: the tables only.  Ids outside [0, E)
+ * other than -1 are empty slots too and set the device error word (SP24_ERR_INVALID_ARG).
+ * The gradient of x is sp24_moe_unsort of xs's gradient with router_w NULL.
+ * n up to 2^31 - 1, E up to 2^20 (SP24_ERR_UNSUPPORTED above).  n == 0 writes offsets only.
+ * workspace: sp24_moe_sort_workspace_size() bytes (may be 0), 16-byte aligned; scratch. */
+int sp24_moe_sort_workspace_size(int64_t T, int topk, int64_t E, int64_t* bytes);
+int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, int64_t T, int topk, int64_t E, int64_t H,
+                  void* xs, int32_t* pos, int32_t* src, int32_t* row_expert, int32_t* offsets, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+
+/* Back in token order, with the router weights applied:  y[t] = sum_s router_w[t, s] ys[pos[t, s]],
+ * summed in fp32 in slot order and rounded once to y's type (empty slots add nothing: a NaN weight
+ * there does not count).
+ *   ys        device [rows, H], F32/F16/BF16;  pos: device int32 [T, topk] from sp24_moe_sort
+ *   router_w  device fp32 [T, topk], or NULL for weights of 1
+ *   y         device [T, H]: ys's type or F32, any type when ys is F32
+ * sp24_moe_unsort_backward, with dy (device, y's type, [T, H]):
+ *   dys[pos[t, s]] = router_w[t, s] dy[t]   (device, ys's type, [rows, H]; other rows are left as
+ *                                            they were)
+ *   d_router_w[t, s] = sum_h dy[t, h] ys[pos[t, s], h]   (device fp32 [T, topk] or NULL; 0 for an
+ *                                            empty slot; ys is read only for this and may be NULL
+ *                                            with it)
+ * A pos outside [0, rows) is an empty slot; other than -1 it sets the device error word
+ * (SP24_ERR_INVALID_ARG).  Two entries of one row (no sort gives that) leave either one's dys.
+ * topk up to 64 (SP24_ERR_UNSUPPORTED above).  One launch each, no workspace. */
+int sp24_moe_unsort(const void* ys, int ys_dtype, const int32_t* pos, const float* router_w, int64_t T, int topk,
+                    int64_t rows, int64_t H, void* y, int y_dtype, void* stream);
+int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void* ys, int ys_dtype, const int32_t* pos,
+                             const float* router_w, int64_t T, int topk, int64_t rows, int64_t H, void* dys,
+                             float* d_router_w, void* stream);
+
+/* ----------------------------------------------------------------------- 4-bit group weights */
+/* Integer 4-bit weights with one scale, and optionally one zero point, per `group` consecutive
+ * entries of a row (not on the source pages, whose 4-bit format is NVFP4; the decode form follows
+ * [P5] "Why NVFP4 helps without FP4 hardware": the weight bytes are what a decode step reads).
+ *   value[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
+ *   codes   device [rows, K/2] bytes, q in 0..15, entry 2i in the low nibble, 16-byte aligned
+ *   scales  device [rows, K/group], F16 or BF16 (scale_dtype), 2-byte aligned
+ *   zeros   device [rows, K/group] bytes, the low four bits are read; NULL: 8 everywhere
+ *   group   32, 64 or 128;  K % group == 0 */
+typedef struct {
+  int32_t scale_dtype;
+  int32_t group;
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+} sp24_w4_operand;
+
+/* Quantise w[rows, K] (device, F16 or BF16, 16-byte aligned), every step IEEE fp32, R() = rounding
+ * to w's type, per group:
+ *   with_zeros == 0:  s = R(max|w| / 7), z = 8
+ *   with_zeros != 0:  lo = min(w, 0), hi = max(w, 0);  s = R((hi - lo) / 15),
+ *                     z = clamp(floor(-lo / s + 1/2), 0, 15)
+ *   q = clamp(floor(w / s + 1/2) + z, 0, 15)   (a quotient halfway between two codes goes up)
+ * An s below 2^-126 is stored as 0, with z = 0 (8 without zero points) and q = z.  Non-finite
+ * entries give unspecified codes in their group.  codes / scales / zeros as above (scales in w's
+ * type; zeros required iff with_zeros).  One launch, no workspace.
+ * sp24_dequantize_w4: out[rows, K] = (q - z) * s rounded once to out_dtype (F16/BF16/F32). */
+int sp24_quantize_w4(const void* w, int dtype, int64_t rows, int64_t K, int group, int with_zeros, uint8_t* codes,
+                     void* scales, uint8_t* zeros, void* stream);
+int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_t K, int out_dtype, void* out, void* stream);
+
+/* Products of a few rows with such weights, for decode:
+ *   v[m, n] = sum_k x[m, k] value[n, k]    (fp32; exact products, summed per group and then scaled)
+ *   sp24_gemv_w4          x device [M, K], one matrix [N, K]
+ *   sp24_gemv_w4_grouped  x device [R, K] in expert order, E matrices stacked as [E N, K], offsets
+ *                         device int32 [E + 1] (sp24_moe_sort): row r in [offsets[e], offsets[e+1])
+ *                         meets matrix e; rows of y from offsets[E] on are left as they were.
+ *                         Offsets are clamped to [0, R]; a descending pair holds no rows.
+ *   x     F16 or BF16, 16-byte aligned; scale_dtype may be the other one of the two.
+ *   act   SP24_ACT_NONE:   y[m, n] = v[m, n], y [M, N]
+ *         SP24_ACT_SWIGLU: N even, the first N/2 rows of a matrix are the gate, the others the up
+ *                          projection: y[m, f] = SiLU(v[m, f]) * v[m, N/2 + f], y [M, N/2];
+ *                          SiLU(g) = g / (1 + e^-g)
+ *   y     device, F32 or x's type (y_dtype)
+ * K / group <= 1024 (SP24_ERR_UNSUPPORTED above).  Any number of rows is served, eight at a time
+ * per read of a weight tile: for more than a few dozen rows use the GEMM entry points.  M == 0,
+ * R == 0 or N == 0 is a no-op; K == 0 writes zeros.  One launch, no workspace, no atomics. */
+enum { SP24_ACT_NONE = 0, SP24_ACT_SWIGLU = 1 };
+int sp24_gemv_w4(const void* x, int x_dtype, const sp24_w4_operand* w, int64_t M, int64_t N, int64_t K, int act,
+                 void* y, int y_dtype, void* stream);
+int sp24_gemv_w4_grouped(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* offsets, int64_t R,
+                         int64_t E, int64_t N, int64_t K, int act, void* y, int y_dtype, void* stream);
+
 /* ----------------------------------------------------------------------- diagnostics */
 /* Number of kernels this library has launched in this process (host-side counter, all
  * devices and streams).  For accounting in benchmarks; memsets are not counted. */

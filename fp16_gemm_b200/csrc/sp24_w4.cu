@@ -120,79 +120,336 @@ struct GemvW4 {
   const int32_t* offsets;  // grouped: E + 1
   void* y;
   int64_t M, E, N, K;
-  int scale_dtype, group, act, y_f32;
+  int scale_dtype, group, y_f32;
+  int wk;       // warps along K (a power of two); the other 8 / wk take further columns
+  int x_rows;   // rows of x a stage has room for
 };
 
-constexpr int kTok = 8;  // rows of x per CTA
+constexpr int kWarps = 8;
+constexpr int kChunk = 128;     // entries of K per stage: 64 code bytes of each row
+constexpr int kTileBytes = 16 * kChunk / 2;
 
-// One warp per output column (with SwiGLU: its gate and its up row), eight rows of x at a time.
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
 template <int XT>
-__global__ void __launch_bounds__(128) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (XT == SP24_BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The code q as a 16-bit float without a conversion: its four bits are or-ed into the significand of
+// 2^10 (f16) or 2^7 (bf16), whose last place is 1, and the same number plus the zero point is
+// subtracted: q - z exactly.  kMagic is that number's bits, in both halves of a word.
+template <int XT>
+constexpr uint32_t kMagic = XT == SP24_BF16 ? 0x43004300u : 0x64006400u;
+
+// (word & mask) | magic, one three-input logic operation.
+__device__ __forceinline__ uint32_t and_or(uint32_t word, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(word), "r"(mask), "r"(magic));
+  return r;
+}
+
+template <int XT>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  if (XT == SP24_BF16) {
+    const __nv_bfloat162 r = __hsub2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(b));
+    return reinterpret_cast<const uint32_t&>(r);
+  }
+  const __half2 r = __hsub2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b));
+  return reinterpret_cast<const uint32_t&>(r);
+}
+
+// The eight codes of a word as four pairs of q - z: entries (0, 4), (1, 5), (2, 6), (3, 7).  `zero` is
+// kMagic + z in both halves.
+template <int XT>
+__device__ __forceinline__ void expand8(uint32_t word, uint32_t zero, uint32_t (&out)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) out[k] = sub2<XT>(and_or(word >> (4 * k), 0x000f000fu, kMagic<XT>), zero);
+}
+
+// Tile `tile` of all experts' tiles of `rows` rows: its expert, first row and end (one warp).
+// Each lane sums the tiles of a contiguous run of experts; the run that holds the tile is then
+// looked through by all lanes.
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int64_t E, int64_t M, int64_t tile,
+                                          int rows, int64_t& e, int64_t& m0, int64_t& m1) {
   const int lane = threadIdx.x & 31;
-  const int64_t cols = p.act == SP24_ACT_SWIGLU ? p.N / 2 : p.N;
-  const int64_t col = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (col >= cols) return;
+  auto tiles_of = [&](int64_t i, int64_t& a, int64_t& b) {
+    a = max(0, offsets[i]);
+    b = min(M, (int64_t)offsets[i + 1]);
+    return b > a ? (b - a + rows - 1) / rows : 0;
+  };
+  auto scan = [&](int64_t v) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(kFull, v, d);
+      if (lane >= d) v += o;
+    }
+    return v;
+  };
+  const int64_t per = (E + 31) / 32;
+  int64_t mine = 0, a, b;
+  for (int64_t i = lane * per; i < min(E, (lane + 1) * per); ++i) mine += tiles_of(i, a, b);
+  int64_t upto = scan(mine);
+  const unsigned past = __ballot_sync(kFull, upto > tile);
+  if (!past) return false;
+  const int who = __ffs(past) - 1;
+  tile -= __shfl_sync(kFull, upto - mine, who);
+  for (int64_t i0 = who * per; i0 < min(E, (who + 1) * per); i0 += 32) {
+    const int64_t i = i0 + lane;
+    mine = i < min(E, (who + 1) * per) ? tiles_of(i, a, b) : 0;
+    upto = scan(mine);
+    const unsigned hit = __ballot_sync(kFull, upto > tile);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      e = i0 + l;
+      const int64_t first = __shfl_sync(kFull, a, l);
+      m1 = __shfl_sync(kFull, b, l);
+      m0 = first + (tile - __shfl_sync(kFull, upto - mine, l)) * rows;
+      return true;
+    }
+    tile -= __shfl_sync(kFull, upto, 31);
+  }
+  return false;
+}
+
+// y = x W^T for up to 8 NT rows of x and MT tiles of 16 weight rows per warp (with SwiGLU: a gate
+// tile and its up tile).  The weight rows are the MMA's M, the rows of x its N.
+//
+// K is split over wk warps of the CTA in chunks of 128 entries; each warp streams its chunks of
+// codes and x through a ring of S stages of its own with cp.async, so nothing in the loop waits
+// for another warp.  An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of
+// a 32-entry block of rows g and g + 8; the MMA may sum K in any order, so the pairs that expand8
+// gives are fed as they come, with x's pairs picked alike.  A group's sum is scaled in fp32; the
+// warps' partial sums meet in shared memory in a fixed order.
+template <int XT, int NT, int MT, int S, bool SWIGLU>
+__global__ void __launch_bounds__(32 * kWarps) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  constexpr int kTok = 8 * NT;
   int64_t e = 0, m0 = (int64_t)blockIdx.y * kTok, m1 = p.M;
-  if (p.offsets) {  // tile blockIdx.y of the tiles of all experts
-    int64_t tile = blockIdx.y;
-    for (e = 0; e < p.E; ++e) {
-      const int64_t a = max(0, p.offsets[e]), b = min(p.M, (int64_t)p.offsets[e + 1]);
-      const int64_t tiles = b > a ? (b - a + kTok - 1) / kTok : 0;
-      if (tile < tiles) {
-        m0 = a + tile * kTok;
-        m1 = b;
-        break;
-      }
-      tile -= tiles;
-    }
-    if (e == p.E) return;
-  }
+  if (p.offsets && !find_tile(p.offsets, p.E, p.M, blockIdx.y, kTok, e, m0, m1)) return;
   const int rows = (int)min((int64_t)kTok, m1 - m0);
+
+  const int wk = p.wk, wn = kWarps / wk;
+  const int kw = warp & (wk - 1), nw = warp / wk;
+  constexpr int kCols = SWIGLU ? 16 : 16 * MT;  // output columns per warp
+  const int64_t cols = SWIGLU ? p.N / 2 : p.N;
+  const int64_t cta_col = (int64_t)blockIdx.x * kCols * wn, col0 = cta_col + nw * kCols;
+  // first weight row of this warp's tile i (clamped rows are computed and not stored)
+  auto tile_row = [&](int i, int r) {
+    const int64_t c = min(col0 + (SWIGLU ? r : 16 * i + r), cols - 1);
+    return e * p.N + (SWIGLU ? i * cols : 0) + c;
+  };
+
   const int64_t KG = p.K / p.group;
-  const uint4* x = reinterpret_cast<const uint4*>(p.x) + m0 * (p.K / 8);
-  float v[2][kTok];
+  const int stride = (int)KG | 1;  // words per row of the scale table: odd, so eight rows are eight banks
+  const int stage_bytes = MT * kTileBytes + p.x_rows * 2 * kChunk;
+  uint8_t* ring = smem + warp * S * stage_bytes;
+  uint32_t* table = reinterpret_cast<uint32_t*>(smem + kWarps * S * stage_bytes) + nw * MT * 16 * stride;
+
+  const int chunks = (int)((p.K + kChunk - 1) / kChunk);
+  const uint8_t* code_src[MT][2];
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    if (part && p.act != SP24_ACT_SWIGLU) break;
-    const int64_t row = e * p.N + part * (p.N / 2) + col;
-    const uint32_t* codes = reinterpret_cast<const uint32_t*>(p.codes + row * (p.K / 2));
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int m = 0; m < kTok; ++m) v[part][m] = 0.0f;
-    for (int64_t c = lane; c < p.K / 8; c += 32) {
-      const uint32_t q = codes[c];
-      const int64_t g = row * KG + c * 8 / p.group;
-      const float s = scale16(p.scales, g, p.scale_dtype);
-      const int z = p.zeros ? p.zeros[g] & 15 : 8;
+    for (int h = 0; h < 2; ++h) code_src[i][h] = p.codes + tile_row(i, (lane >> 2) + 8 * h) * (p.K / 2) + 16 * t;
+  const uint8_t* x_src = reinterpret_cast<const uint8_t*>(p.x) + m0 * p.K * 2;
+  const int row_sw = ((lane >> 2) >> 1) & 3;  // rows r and r + 8 swizzle alike
+
+  auto fetch = [&](int c, int slot) {
+    const uint32_t dst = smem_addr(ring + slot * stage_bytes);
+    const int64_t k0 = (int64_t)c * kChunk;
+    if (k0 + 32 * t < p.K) {
 #pragma unroll
-      for (int m = 0; m < kTok; ++m) {
-        if (m >= rows) break;
-        const uint4 xv = x[m * (p.K / 8) + c];
-        const uint32_t word[4] = {xv.x, xv.y, xv.z, xv.w};
-        float sum = 0.0f;
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sum = fmaf((float)((int)(q >> (8 * k) & 15) - z), Half16<XT>::get(word[k] & 0xffffu), sum);
-          sum = fmaf((float)((int)(q >> (8 * k + 4) & 15) - z), Half16<XT>::get(word[k] >> 16), sum);
+        for (int h = 0; h < 2; ++h)
+          copy16(dst + i * kTileBytes + ((lane >> 2) + 8 * h) * 64 + 16 * (t ^ row_sw), code_src[i][h] + k0 / 2);
+    }
+    // x: row m's 256 bytes at 256 m, its 16-byte piece j at 16 (j ^ 4 (m & 1))
+    for (int j = lane; j < rows * 16; j += 32) {
+      const int m = j >> 4, piece = j & 15;
+      if (k0 + 8 * piece < p.K)
+        copy16(dst + MT * kTileBytes + m * 256 + 16 * (piece ^ (m & 1) * 4), x_src + m * p.K * 2 + (k0 + 8 * piece) * 2);
+    }
+  };
+
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    if (kw + s * wk < chunks) fetch(kw + s * wk, s);
+    copy_commit();
+  }
+  // the scale of (row, group) beside kMagic + its zero point, one word
+  for (int r = kw; r < MT * 16; r += wk) {
+    const int64_t row = tile_row(r >> 4, r & 15) * KG;
+    for (int64_t k = lane; k < KG; k += 32) {
+      const uint32_t z = p.zeros ? p.zeros[row + k] & 15u : 8u;
+      table[r * stride + k] = p.scales[row + k] | ((kMagic<XT> >> 16) + z) << 16;
+    }
+  }
+  __syncthreads();
+
+  float tot[MT][NT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tot[i][n][k] = 0.0f;
+  float acc[MT][NT][4] = {};
+  const int blocks_per_group = p.group / 32;
+
+  // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4)
+  const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
+  int slot = 0;
+  for (int c = kw; c < chunks; c += wk) {
+    copy_wait<S - 1>();
+    __syncwarp();
+    const uint8_t* stage = ring + slot * stage_bytes;
+    const uint8_t* xs = stage + MT * kTileBytes;
+    const int64_t k0 = (int64_t)c * kChunk;
+    const int blocks = (int)min((int64_t)4, (p.K - k0) / 32);
+#pragma unroll
+    for (int jj = 0; jj < 4; jj += 2) {
+      uint32_t words[MT][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        ldmatrix4(words[i], smem_addr(stage + i * kTileBytes + lm_row * 64 + 16 * ((jj + (lane >> 4)) ^ (lm_row >> 1 & 3))));
+#pragma unroll
+      for (int jb = 0; jb < 2; ++jb) {
+        const int j = jj + jb;
+        if (j >= blocks) break;
+        const int64_t grp = (k0 / 32 + j) / blocks_per_group;
+        uint32_t b[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int m = min(8 * n + g, rows - 1);  // columns past the last row are not stored
+          const uint4 v = *reinterpret_cast<const uint4*>(xs + m * 256 + 16 * ((4 * j + t) ^ (m & 1) * 4));
+          b[n][0] = __byte_perm(v.x, v.z, 0x5410);
+          b[n][1] = __byte_perm(v.x, v.z, 0x7632);
+          b[n][2] = __byte_perm(v.y, v.w, 0x5410);
+          b[n][3] = __byte_perm(v.y, v.w, 0x7632);
         }
-        v[part][m] = fmaf(s, sum, v[part][m]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint32_t tl = table[(16 * i + g) * stride + grp], th = table[(16 * i + g + 8) * stride + grp];
+          uint32_t lo[4], hi[4];
+          expand8<XT>(words[i][2 * jb], __byte_perm(tl, tl, 0x3232), lo);
+          expand8<XT>(words[i][2 * jb + 1], __byte_perm(th, th, 0x3232), hi);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t a[4] = {lo[2 * half], hi[2 * half], lo[2 * half + 1], hi[2 * half + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<XT>(acc[i][n], a, b[n][2 * half], b[n][2 * half + 1]);
+          }
+          if ((k0 / 32 + j + 1) % blocks_per_group == 0) {
+            const float sl = p.scale_dtype == SP24_BF16 ? Half16<SP24_BF16>::get(tl & 0xffffu) : Half16<SP24_F16>::get(tl & 0xffffu);
+            const float sh = p.scale_dtype == SP24_BF16 ? Half16<SP24_BF16>::get(th & 0xffffu) : Half16<SP24_F16>::get(th & 0xffffu);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                tot[i][n][k] = fmaf(k < 2 ? sl : sh, acc[i][n][k], tot[i][n][k]);
+                acc[i][n][k] = 0.0f;
+              }
+          }
+        }
       }
     }
-#pragma unroll
-    for (int m = 0; m < kTok; ++m)
-#pragma unroll
-      for (int d = 16; d; d >>= 1) v[part][m] += __shfl_xor_sync(kFull, v[part][m], d);
+    __syncwarp();
+    if (c + S * wk < chunks) fetch(c + S * wk, slot);
+    copy_commit();
+    slot = slot + 1 == S ? 0 : slot + 1;
   }
+  copy_wait<0>();
+  __syncthreads();  // every warp is past its ring: the partial sums take its place
+
+  // partial[warp][tile][token][row]
+  float* partial = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int m = 0; m < kTok; ++m) {
-    if (m != lane || m >= rows) continue;
-    float out = v[0][m];
-    if (p.act == SP24_ACT_SWIGLU) out = out / (1.0f + expf(-out)) * v[1][m];
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        partial[((warp * MT + i) * kTok + 8 * n + 2 * t + (k & 1)) * 16 + g + 8 * (k >> 1)] = tot[i][n][k];
+  __syncthreads();
+  const int per_warp_cols = SWIGLU ? 1 : MT;
+  for (int o = threadIdx.x; o < wn * per_warp_cols * kTok * 16; o += 32 * kWarps) {
+    const int r = o & 15, i = (o >> 4) % per_warp_cols, w = (o >> 4) / per_warp_cols % wn, m = o / (16 * per_warp_cols * wn);
+    const int64_t col = cta_col + (w * per_warp_cols + i) * 16 + r;
+    if (m >= rows || col >= cols) continue;
+    float v = 0.0f, up = 0.0f;
+    for (int k = 0; k < wk; ++k) {
+      v += partial[(((w * wk + k) * MT + i) * kTok + m) * 16 + r];
+      if (SWIGLU) up += partial[(((w * wk + k) * MT + 1) * kTok + m) * 16 + r];
+    }
+    if (SWIGLU) v = v / (1.0f + expf(-v)) * up;
     const int64_t at = (m0 + m) * cols + col;
     if (p.y_f32)
-      reinterpret_cast<float*>(p.y)[at] = out;
+      reinterpret_cast<float*>(p.y)[at] = v;
     else
-      reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)Half16<XT>::put(out);
+      reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)Half16<XT>::put(v);
   }
+}
+
+template <int XT, int NT, int MT, int S, bool SWIGLU>
+int launch_gemv(const GemvW4& p, int64_t tiles, cudaStream_t s) {
+  const int wn = kWarps / p.wk;
+  const int64_t cols = SWIGLU ? p.N / 2 : p.N, per_cta = (int64_t)(SWIGLU ? 16 : 16 * MT) * wn;
+  const int ring = kWarps * S * (MT * kTileBytes + p.x_rows * 2 * kChunk);
+  const int bytes = ring + wn * MT * 16 * ((int)(p.K / p.group) | 1) * 4;
+  static bool raised[64];  // the attribute holds per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SP24_ERR_CUDA;
+  if (dev < 0 || dev >= 64 || !raised[dev]) {
+    if (cudaFuncSetAttribute(gemv_w4_kernel<XT, NT, MT, S, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             232448) != cudaSuccess)
+      return SP24_ERR_CUDA;
+    if (dev >= 0 && dev < 64) raised[dev] = true;
+  }
+  gemv_w4_kernel<XT, NT, MT, S, SWIGLU>
+      <<<dim3((unsigned)((cols + per_cta - 1) / per_cta), (unsigned)tiles), 32 * kWarps, bytes, s>>>(p);
+  return launch_status();
+}
+
+template <int XT>
+int by_shape(GemvW4& p, bool grouped, int act, cudaStream_t s) {
+  const int64_t chunks = (p.K + kChunk - 1) / kChunk;
+  p.wk = chunks >= 8 ? 8 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+  // sixteen rows of x per tile only where eight would leave a second tile per matrix
+  const bool wide = grouped ? p.M > 8 * p.E : p.M > 8;
+  const int tok = wide ? 16 : 8;
+  p.x_rows = (int)(p.M < tok ? p.M : tok);
+  // grouped: the sum over experts of ceil(rows / tok) is at most this
+  const int64_t tiles = (p.M + tok - 1) / tok + (grouped ? (p.E < p.M ? p.E : p.M) : 0);
+  if (tiles > 65535) return SP24_ERR_UNSUPPORTED;
+  if (act == SP24_ACT_SWIGLU)
+    return wide ? launch_gemv<XT, 2, 2, 2, true>(p, tiles, s) : launch_gemv<XT, 1, 2, 2, true>(p, tiles, s);
+  if (wide) return launch_gemv<XT, 2, 2, 2, false>(p, tiles, s);
+  return p.x_rows > 2 ? launch_gemv<XT, 1, 2, 2, false>(p, tiles, s) : launch_gemv<XT, 1, 1, 4, false>(p, tiles, s);
 }
 
 bool is16(int d) { return d == SP24_F16 || d == SP24_BF16; }
@@ -220,17 +477,9 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   if (K == 0) return cudaMemsetAsync(y, 0, (size_t)(M * cols * yb), s) == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
   if (!x || !w->codes || !w->scales) return SP24_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 2)) return SP24_ERR_ALIGN;
-  // grouped: sum over experts of ceil(rows / 8) tiles, at most this many
-  const int64_t tiles = grouped ? (M + kTok - 1) / kTok + (E < M ? E : M) : (M + kTok - 1) / kTok;
-  if (tiles > 65535) return SP24_ERR_UNSUPPORTED;
   GemvW4 p{x, w->codes, reinterpret_cast<const uint16_t*>(w->scales), w->zeros, grouped ? offsets : nullptr, y,
-           M, E, N, K, w->scale_dtype, w->group, act, y_dtype == SP24_F32};
-  const dim3 grid((unsigned)((cols + 3) / 4), (unsigned)tiles);
-  if (x_dtype == SP24_BF16)
-    gemv_w4_kernel<SP24_BF16><<<grid, 128, 0, s>>>(p);
-  else
-    gemv_w4_kernel<SP24_F16><<<grid, 128, 0, s>>>(p);
-  return launch_status();
+           M, E, N, K, w->scale_dtype, w->group, y_dtype == SP24_F32, 0, 0};
+  return x_dtype == SP24_BF16 ? by_shape<SP24_BF16>(p, grouped, act, s) : by_shape<SP24_F16>(p, grouped, act, s);
 }
 
 unsigned stream_ctas(int64_t vecs) {

@@ -121,8 +121,8 @@ struct GemvW4 {
   void* y;
   int64_t M, E, N, K;
   int scale_dtype, group, y_f32;
-  int wk;       // warps along K (a power of two); the other 8 / wk take further columns
-  int x_rows;   // rows of x a stage has room for
+  int wk;      // warps along K (a power of two); the other 8 / wk take further columns
+  int x_rows;  // rows of x that shared memory has room for
 };
 
 constexpr int kWarps = 8;
@@ -237,12 +237,15 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
 // tile and its up tile).  The weight rows are the MMA's M, the rows of x its N.
 //
 // K is split over wk warps of the CTA in chunks of 128 entries; each warp streams its chunks of
-// codes and x through a ring of S stages of its own with cp.async, so nothing in the loop waits
-// for another warp.  An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of
+// codes through a ring of S stages of its own with cp.async, so nothing in the loop waits for
+// another warp.  An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of
 // a 32-entry block of rows g and g + 8; the MMA may sum K in any order, so the pairs that expand8
 // gives are fed as they come, with x's pairs picked alike.  A group's sum is scaled in fp32; the
 // warps' partial sums meet in shared memory in a fixed order.
-template <int XT, int NT, int MT, int S, bool SWIGLU>
+//
+// XW: x stands in shared memory whole, its pairs picked when it is brought there (few rows of x);
+// otherwise its chunk travels in the ring and the pairs are picked at each use.
+template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
 __global__ void __launch_bounds__(32 * kWarps) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -257,42 +260,92 @@ __global__ void __launch_bounds__(32 * kWarps) gemv_w4_kernel(const __grid_const
   constexpr int kCols = SWIGLU ? 16 : 16 * MT;  // output columns per warp
   const int64_t cols = SWIGLU ? p.N / 2 : p.N;
   const int64_t cta_col = (int64_t)blockIdx.x * kCols * wn, col0 = cta_col + nw * kCols;
-  // first weight row of this warp's tile i (clamped rows are computed and not stored)
+  // weight row r of this warp's tile i (rows past the end: the last one, computed and not stored)
   auto tile_row = [&](int i, int r) {
     const int64_t c = min(col0 + (SWIGLU ? r : 16 * i + r), cols - 1);
     return e * p.N + (SWIGLU ? i * cols : 0) + c;
   };
+  const int K = (int)p.K, KG = K / (32 * GB);
+  const int chunks = (K + kChunk - 1) / kChunk;
 
-  const int64_t KG = p.K / p.group;
-  const int stride = (int)KG | 1;  // words per row of the scale table: odd, so eight rows are eight banks
-  const int stage_bytes = MT * kTileBytes + p.x_rows * 2 * kChunk;
-  uint8_t* ring = smem + warp * S * stage_bytes;
-  uint32_t* table = reinterpret_cast<uint32_t*>(smem + kWarps * S * stage_bytes) + nw * MT * 16 * stride;
+  constexpr int kGroups = 4 / GB;                       // groups per chunk
+  constexpr int kScales = 16 * MT * kGroups;            // of all rows
+  constexpr int kPer = (kScales + 31) / 32;             // per lane
+  constexpr int kWord = ZEROS ? 8 : 4;                  // the scale, and the zero point beside it
+  const int stage_bytes = MT * kTileBytes + (XW ? 0 : p.x_rows * 2 * kChunk);
+  const int warp_bytes = S * stage_bytes + 2 * kScales * kWord;
+  uint8_t* ring = smem + warp * warp_bytes;
+  uint8_t* table = ring + S * stage_bytes;
+  uint8_t* x_all = smem + kWarps * warp_bytes;
+  const int x_stride = (2 * K + 127) / 128 * 128 + 64;  // two neighbouring rows of x never meet in a bank
 
-  const int chunks = (int)((p.K + kChunk - 1) / kChunk);
   const uint8_t* code_src[MT][2];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) code_src[i][h] = p.codes + tile_row(i, (lane >> 2) + 8 * h) * (p.K / 2) + 16 * t;
+    for (int h = 0; h < 2; ++h)
+      code_src[i][h] = p.codes + tile_row(i, g + 8 * h) * (p.K / 2) + 16 * t + kw * (kChunk / 2);
   const uint8_t* x_src = reinterpret_cast<const uint8_t*>(p.x) + m0 * p.K * 2;
-  const int row_sw = ((lane >> 2) >> 1) & 3;  // rows r and r + 8 swizzle alike
+  const uint32_t ring_at = smem_addr(ring);
+  const uint32_t code_dst = ring_at + g * 64 + 16 * (t ^ (g >> 1 & 3));  // rows g and g + 8 swizzle alike
 
-  auto fetch = [&](int c, int slot) {
-    const uint32_t dst = smem_addr(ring + slot * stage_bytes);
-    const int64_t k0 = (int64_t)c * kChunk;
-    if (k0 + 32 * t < p.K) {
+  auto fetch = [&](int c, int slot) {  // chunks in order: the sources move on with each call
+    const int k0 = c * kChunk;
+    const uint32_t dst = code_dst + slot * stage_bytes;
+    if (k0 + 32 * t < K) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          copy16(dst + i * kTileBytes + ((lane >> 2) + 8 * h) * 64 + 16 * (t ^ row_sw), code_src[i][h] + k0 / 2);
+        for (int h = 0; h < 2; ++h) copy16(dst + i * kTileBytes + h * 512, code_src[i][h]);
     }
-    // x: row m's 256 bytes at 256 m, its 16-byte piece j at 16 (j ^ 4 (m & 1))
-    for (int j = lane; j < rows * 16; j += 32) {
-      const int m = j >> 4, piece = j & 15;
-      if (k0 + 8 * piece < p.K)
-        copy16(dst + MT * kTileBytes + m * 256 + 16 * (piece ^ (m & 1) * 4), x_src + m * p.K * 2 + (k0 + 8 * piece) * 2);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) code_src[i][h] += wk * (kChunk / 2);
+    if (!XW) {  // x: row m's 256 bytes at 256 m, its 16-byte piece j at 16 (j ^ 4 (m & 1))
+      const uint32_t xdst = ring_at + slot * stage_bytes + MT * kTileBytes;
+      for (int j = lane; j < rows * 16; j += 32) {
+        const int m = j >> 4, piece = j & 15;
+        if (k0 + 8 * piece < K)
+          copy16(xdst + m * 256 + 16 * (piece ^ (m & 1) * 4), x_src + ((int64_t)m * K + k0 + 8 * piece) * 2);
+      }
+    }
+  };
+
+  // scales (and zero points) of a chunk: one chunk ahead in registers, then in a table of two turns
+  int64_t scale_at[kPer];
+  int scale_group[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = lane + 32 * i, r = s / kGroups;
+    scale_group[i] = s < kScales ? kw * kGroups + s % kGroups : KG;
+    scale_at[i] = tile_row(r >> 4 & (MT - 1), r & 15) * KG + scale_group[i];
+  }
+  uint32_t scale_bits[kPer], zero_bits[kPer];
+  auto load_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      scale_bits[i] = 0;
+      zero_bits[i] = 8;
+      if (scale_group[i] < KG) {
+        scale_bits[i] = p.scales[scale_at[i]];
+        if (ZEROS) zero_bits[i] = p.zeros[scale_at[i]];
+      }
+      scale_group[i] += wk * kGroups;
+      scale_at[i] += wk * kGroups;
+    }
+  };
+  auto put_scales = [&](int turn) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int s = lane + 32 * i;
+      if (s >= kScales) break;
+      const float v = p.scale_dtype == SP24_BF16 ? Half16<SP24_BF16>::get(scale_bits[i]) : Half16<SP24_F16>::get(scale_bits[i]);
+      if (ZEROS)
+        reinterpret_cast<uint2*>(table)[turn * kScales + s] =
+            make_uint2(__float_as_uint(v), kMagic<XT> + (zero_bits[i] & 15u) * 0x10001u);
+      else
+        reinterpret_cast<float*>(table)[turn * kScales + s] = v;
     }
   };
 
@@ -301,72 +354,94 @@ __global__ void __launch_bounds__(32 * kWarps) gemv_w4_kernel(const __grid_const
     if (kw + s * wk < chunks) fetch(kw + s * wk, s);
     copy_commit();
   }
-  // the scale of (row, group) beside kMagic + its zero point, one word
-  for (int r = kw; r < MT * 16; r += wk) {
-    const int64_t row = tile_row(r >> 4, r & 15) * KG;
-    for (int64_t k = lane; k < KG; k += 32) {
-      const uint32_t z = p.zeros ? p.zeros[row + k] & 15u : 8u;
-      table[r * stride + k] = p.scales[row + k] | ((kMagic<XT> >> 16) + z) << 16;
-    }
+  load_scales();
+  if (XW) {
+    const int pieces = K / 8;
+    for (int m = 0; m < rows; ++m)
+      for (int j = threadIdx.x; j < pieces; j += 32 * kWarps) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x_src) + (int64_t)m * pieces + j);
+        *reinterpret_cast<uint4*>(x_all + m * x_stride + 16 * j) =
+            make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                       __byte_perm(v.y, v.w, 0x7632));
+      }
+    __syncthreads();
   }
-  __syncthreads();
 
   float tot[MT][NT][4];
+  float acc[MT][NT][4];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tot[i][n][k] = 0.0f;
-  float acc[MT][NT][4] = {};
-  const int blocks_per_group = p.group / 32;
+      for (int k = 0; k < 4; ++k) tot[i][n][k] = acc[i][n][k] = 0.0f;
 
   // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4)
   const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
-  int slot = 0;
+  const uint32_t lm_at = ring_at + lm_row * 64;
+  const int lm_sw = lm_row >> 1 & 3, lm_block = lane >> 4;
+  const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
+  int x_flip[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int m = min(8 * n + g, rows - 1);
+    x_row[n] = XW ? x_all + m * x_stride + 16 * t : ring + MT * kTileBytes + m * 256 + 16 * t;
+    x_flip[n] = (m & 1) * 64;
+  }
+
+  int slot = 0, turn = 0;
   for (int c = kw; c < chunks; c += wk) {
+    put_scales(turn);
+    load_scales();
     copy_wait<S - 1>();
     __syncwarp();
-    const uint8_t* stage = ring + slot * stage_bytes;
-    const uint8_t* xs = stage + MT * kTileBytes;
-    const int64_t k0 = (int64_t)c * kChunk;
-    const int blocks = (int)min((int64_t)4, (p.K - k0) / 32);
+    const int blocks = min(4, K / 32 - 4 * c);
 #pragma unroll
     for (int jj = 0; jj < 4; jj += 2) {
+      if (jj >= blocks) break;
       uint32_t words[MT][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-        ldmatrix4(words[i], smem_addr(stage + i * kTileBytes + lm_row * 64 + 16 * ((jj + (lane >> 4)) ^ (lm_row >> 1 & 3))));
+        ldmatrix4(words[i], lm_at + slot * stage_bytes + i * kTileBytes + 16 * ((jj + lm_block) ^ lm_sw));
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb) {
         const int j = jj + jb;
         if (j >= blocks) break;
-        const int64_t grp = (k0 / 32 + j) / blocks_per_group;
         uint32_t b[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const int m = min(8 * n + g, rows - 1);  // columns past the last row are not stored
-          const uint4 v = *reinterpret_cast<const uint4*>(xs + m * 256 + 16 * ((4 * j + t) ^ (m & 1) * 4));
-          b[n][0] = __byte_perm(v.x, v.z, 0x5410);
-          b[n][1] = __byte_perm(v.x, v.z, 0x7632);
-          b[n][2] = __byte_perm(v.y, v.w, 0x5410);
-          b[n][3] = __byte_perm(v.y, v.w, 0x7632);
+          if (XW) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x_row[n] + c * 256 + 64 * j);
+            b[n][0] = v.x, b[n][1] = v.y, b[n][2] = v.z, b[n][3] = v.w;
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(x_row[n] + slot * stage_bytes + (64 * j ^ x_flip[n]));
+            b[n][0] = __byte_perm(v.x, v.z, 0x5410);
+            b[n][1] = __byte_perm(v.x, v.z, 0x7632);
+            b[n][2] = __byte_perm(v.y, v.w, 0x5410);
+            b[n][3] = __byte_perm(v.y, v.w, 0x7632);
+          }
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const uint32_t tl = table[(16 * i + g) * stride + grp], th = table[(16 * i + g + 8) * stride + grp];
+          float sl, sh;
+          uint32_t zl = kMagic<XT> + 0x80008u, zh = zl;
+          const int at = turn * kScales + (16 * i + g) * kGroups + j / GB;
+          if (ZEROS) {
+            const uint2 l = reinterpret_cast<const uint2*>(table)[at], h = reinterpret_cast<const uint2*>(table)[at + 8 * kGroups];
+            sl = __uint_as_float(l.x), zl = l.y, sh = __uint_as_float(h.x), zh = h.y;
+          } else {
+            sl = reinterpret_cast<const float*>(table)[at], sh = reinterpret_cast<const float*>(table)[at + 8 * kGroups];
+          }
           uint32_t lo[4], hi[4];
-          expand8<XT>(words[i][2 * jb], __byte_perm(tl, tl, 0x3232), lo);
-          expand8<XT>(words[i][2 * jb + 1], __byte_perm(th, th, 0x3232), hi);
+          expand8<XT>(words[i][2 * jb], zl, lo);
+          expand8<XT>(words[i][2 * jb + 1], zh, hi);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const uint32_t a[4] = {lo[2 * half], hi[2 * half], lo[2 * half + 1], hi[2 * half + 1]};
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816<XT>(acc[i][n], a, b[n][2 * half], b[n][2 * half + 1]);
           }
-          if ((k0 / 32 + j + 1) % blocks_per_group == 0) {
-            const float sl = p.scale_dtype == SP24_BF16 ? Half16<SP24_BF16>::get(tl & 0xffffu) : Half16<SP24_F16>::get(tl & 0xffffu);
-            const float sh = p.scale_dtype == SP24_BF16 ? Half16<SP24_BF16>::get(th & 0xffffu) : Half16<SP24_F16>::get(th & 0xffffu);
+          if ((j + 1) % GB == 0) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -382,6 +457,7 @@ __global__ void __launch_bounds__(32 * kWarps) gemv_w4_kernel(const __grid_const
     if (c + S * wk < chunks) fetch(c + S * wk, slot);
     copy_commit();
     slot = slot + 1 == S ? 0 : slot + 1;
+    turn ^= 1;
   }
   copy_wait<0>();
   __syncthreads();  // every warp is past its ring: the partial sums take its place
@@ -396,10 +472,11 @@ __global__ void __launch_bounds__(32 * kWarps) gemv_w4_kernel(const __grid_const
       for (int k = 0; k < 4; ++k)
         partial[((warp * MT + i) * kTok + 8 * n + 2 * t + (k & 1)) * 16 + g + 8 * (k >> 1)] = tot[i][n][k];
   __syncthreads();
-  const int per_warp_cols = SWIGLU ? 1 : MT;
-  for (int o = threadIdx.x; o < wn * per_warp_cols * kTok * 16; o += 32 * kWarps) {
-    const int r = o & 15, i = (o >> 4) % per_warp_cols, w = (o >> 4) / per_warp_cols % wn, m = o / (16 * per_warp_cols * wn);
-    const int64_t col = cta_col + (w * per_warp_cols + i) * 16 + r;
+  constexpr int kOutTiles = SWIGLU ? 1 : MT;
+  for (int o = threadIdx.x; o < wn * kOutTiles * kTok * 16; o += 32 * kWarps) {
+    const int r = o & 15, tile = (o >> 4) % (kOutTiles * wn), m = (o >> 4) / (kOutTiles * wn);
+    const int i = tile % kOutTiles, w = tile / kOutTiles;
+    const int64_t col = cta_col + tile * 16 + r;
     if (m >= rows || col >= cols) continue;
     float v = 0.0f, up = 0.0f;
     for (int k = 0; k < wk; ++k) {
@@ -415,24 +492,36 @@ __global__ void __launch_bounds__(32 * kWarps) gemv_w4_kernel(const __grid_const
   }
 }
 
-template <int XT, int NT, int MT, int S, bool SWIGLU>
+template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
 int launch_gemv(const GemvW4& p, int64_t tiles, cudaStream_t s) {
+  auto kernel = gemv_w4_kernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>;
   const int wn = kWarps / p.wk;
   const int64_t cols = SWIGLU ? p.N / 2 : p.N, per_cta = (int64_t)(SWIGLU ? 16 : 16 * MT) * wn;
-  const int ring = kWarps * S * (MT * kTileBytes + p.x_rows * 2 * kChunk);
-  const int bytes = ring + wn * MT * 16 * ((int)(p.K / p.group) | 1) * 4;
+  const int64_t stage = MT * kTileBytes + (XW ? 0 : p.x_rows * 2 * kChunk);
+  const int64_t ring = kWarps * (S * stage + 2 * 16 * MT * (4 / GB) * (ZEROS ? 8 : 4));
+  const int64_t bytes = ring + (XW ? p.x_rows * ((2 * p.K + 127) / 128 * 128 + 64) : 0);
   static bool raised[64];  // the attribute holds per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SP24_ERR_CUDA;
   if (dev < 0 || dev >= 64 || !raised[dev]) {
-    if (cudaFuncSetAttribute(gemv_w4_kernel<XT, NT, MT, S, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             232448) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess)
       return SP24_ERR_CUDA;
     if (dev >= 0 && dev < 64) raised[dev] = true;
   }
-  gemv_w4_kernel<XT, NT, MT, S, SWIGLU>
-      <<<dim3((unsigned)((cols + per_cta - 1) / per_cta), (unsigned)tiles), 32 * kWarps, bytes, s>>>(p);
+  kernel<<<dim3((unsigned)((cols + per_cta - 1) / per_cta), (unsigned)tiles), 32 * kWarps, (size_t)bytes, s>>>(p);
   return launch_status();
+}
+
+template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW>
+int by_group(const GemvW4& p, int64_t tiles, cudaStream_t s) {
+  if (p.zeros) {
+    if (p.group == 128) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, true, 4>(p, tiles, s);
+    if (p.group == 64) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, true, 2>(p, tiles, s);
+    return launch_gemv<XT, NT, MT, S, SWIGLU, XW, true, 1>(p, tiles, s);
+  }
+  if (p.group == 128) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, false, 4>(p, tiles, s);
+  if (p.group == 64) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, false, 2>(p, tiles, s);
+  return launch_gemv<XT, NT, MT, S, SWIGLU, XW, false, 1>(p, tiles, s);
 }
 
 template <int XT>
@@ -446,10 +535,13 @@ int by_shape(GemvW4& p, bool grouped, int act, cudaStream_t s) {
   // grouped: the sum over experts of ceil(rows / tok) is at most this
   const int64_t tiles = (p.M + tok - 1) / tok + (grouped ? (p.E < p.M ? p.E : p.M) : 0);
   if (tiles > 65535) return SP24_ERR_UNSUPPORTED;
-  if (act == SP24_ACT_SWIGLU)
-    return wide ? launch_gemv<XT, 2, 2, 2, true>(p, tiles, s) : launch_gemv<XT, 1, 2, 2, true>(p, tiles, s);
-  if (wide) return launch_gemv<XT, 2, 2, 2, false>(p, tiles, s);
-  return p.x_rows > 2 ? launch_gemv<XT, 1, 2, 2, false>(p, tiles, s) : launch_gemv<XT, 1, 1, 4, false>(p, tiles, s);
+  const bool whole = p.x_rows * p.K <= 16384;  // at most 32 KB of shared memory for x
+  if (act == SP24_ACT_SWIGLU) {
+    if (wide) return by_group<XT, 2, 2, 2, true, false>(p, tiles, s);
+    return whole ? by_group<XT, 1, 2, 2, true, true>(p, tiles, s) : by_group<XT, 1, 2, 2, true, false>(p, tiles, s);
+  }
+  if (wide) return by_group<XT, 2, 2, 2, false, false>(p, tiles, s);
+  return whole ? by_group<XT, 1, 1, 4, false, true>(p, tiles, s) : by_group<XT, 1, 2, 2, false, false>(p, tiles, s);
 }
 
 bool is16(int d) { return d == SP24_F16 || d == SP24_BF16; }
@@ -468,7 +560,7 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   const int st = check_w4(N, K, w->group);
   if (st) return st;
   if (M < 0 || E < 1 || (act == SP24_ACT_SWIGLU && N % 2)) return SP24_ERR_SHAPE;
-  if (M > INT32_MAX || E > INT32_MAX || N > INT32_MAX || K / w->group > 1024) return SP24_ERR_UNSUPPORTED;
+  if (M > INT32_MAX || E > INT32_MAX || N > INT32_MAX || K > INT32_MAX / 2) return SP24_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return SP24_OK;
   const int64_t cols = act == SP24_ACT_SWIGLU ? N / 2 : N;
   const int yb = elem_bytes(y_dtype);

@@ -1,0 +1,38 @@
+// Products of a few rows with 4-bit group weights (sp24_gemv_w4, sp24_gemv_w4_grouped): the kernel
+// and its launch for one type of x.  sp24_w4.cu checks the arguments.
+#pragma once
+
+#include "sp24_internal.cuh"
+
+namespace sp24 {
+
+template <int DT>
+struct W4Half;
+template <>
+struct W4Half<SP24_BF16> {
+  static __device__ __forceinline__ float get(uint32_t h) { return __uint_as_float(h << 16); }
+  static __device__ __forceinline__ uint32_t put(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+};
+template <>
+struct W4Half<SP24_F16> {
+  static __device__ __forceinline__ float get(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
+  static __device__ __forceinline__ uint32_t put(float v) { return __half_as_ushort(__float2half_rn(v)); }
+};
+
+struct GemvW4 {
+  const void* x;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  const int32_t* offsets;  // grouped: E + 1
+  void* y;
+  int64_t M, E, N, K;
+  int scale_dtype, group, act, y_f32;
+  int wk;      // warps along K (a power of two); the other 8 / wk take further columns
+  int x_rows;  // rows of x that shared memory has room for
+};
+
+int gemv_w4_bf16(GemvW4 p, cudaStream_t s);
+int gemv_w4_f16(GemvW4 p, cudaStream_t s);
+
+}  // namespace sp24

@@ -581,8 +581,9 @@ int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void* ys, int ys
  * [P5] "Why NVFP4 helps without FP4 hardware": the weight bytes are what a decode step reads).
  *   value[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
  *   codes   device [rows, K/2] bytes, q in 0..15, entry 2i in the low nibble, 16-byte aligned
- *   scales  device [rows, K/group], F16 or BF16 (scale_dtype), 2-byte aligned
- *   zeros   device [rows, K/group] bytes, the low four bits are read; NULL: 8 everywhere
+ *   scales  device [rows, K/group], F16 or BF16 (scale_dtype), 4-byte aligned
+ *   zeros   device [rows, K/group] bytes, 4-byte aligned, the low four bits are read; NULL: 8
+ *           everywhere
  *   group   32, 64 or 128;  K % group == 0 */
 typedef struct {
   int32_t scale_dtype;
@@ -619,8 +620,8 @@ int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_t K, int ou
  *                          projection: y[m, f] = SiLU(v[m, f]) * v[m, N/2 + f], y [M, N/2];
  *                          SiLU(g) = g / (1 + e^-g)
  *   y     device, F32 or x's type (y_dtype)
- * Any number of rows is served, up to sixteen per read of a weight tile (SP24_ERR_UNSUPPORTED past
- * 65535 such tiles): for more than a few dozen rows use the GEMM entry points.  M == 0,
+ * Any number of rows is served, up to sixteen per read of a weight tile: for more than a few dozen
+ * rows use the GEMM entry points.  K up to 2^30 (SP24_ERR_UNSUPPORTED above).  M == 0,
  * R == 0 or N == 0 is a no-op; K == 0 writes zeros.  One launch, no workspace, no atomics. */
 enum { SP24_ACT_NONE = 0, SP24_ACT_SWIGLU = 1 };
 int sp24_gemv_w4(const void* x, int x_dtype, const sp24_w4_operand* w, int64_t M, int64_t N, int64_t K, int act,

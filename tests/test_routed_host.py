@@ -90,7 +90,7 @@ def test_gemv_w4_refusals(grouped):
     assert f(act=2) == f(x=None) == f(y=None) == f(_op(codes=None)) == f(_op(scales=None)) == sp.ERR_INVALID_ARG
     assert f(_op(group=96)) == f(K=2**30) == f(M=2**31) == f(N=2**31) == sp.ERR_UNSUPPORTED
     assert f(K=192) == f(K=-128) == f(M=-1) == f(N=-1) == f(N=5, act=1) == sp.ERR_SHAPE
-    assert f(x=24) == f(y=18) == f(_op(codes=24)) == f(_op(scales=17)) == sp.ERR_ALIGN
+    assert f(x=24) == f(y=18) == f(_op(codes=24)) == f(_op(scales=18)) == f(_op(zeros=18)) == sp.ERR_ALIGN
     assert f(M=0, x=None, y=None) == f(N=0, y=None) == sp.OK
     if grouped:
         assert f(E=0) == sp.ERR_SHAPE and f(off=None) == sp.ERR_INVALID_ARG and f(off=18) == sp.ERR_ALIGN

@@ -113,7 +113,7 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   const int st = check_w4(N, K, w->group);
   if (st) return st;
   if (M < 0 || E < 1 || (act == SP24_ACT_SWIGLU && N % 2)) return SP24_ERR_SHAPE;
-  if (M > INT32_MAX || E > INT32_MAX || N > INT32_MAX || K > INT32_MAX / 2) return SP24_ERR_UNSUPPORTED;
+  if (M > INT32_MAX || E > INT32_MAX || N > INT32_MAX || K > (1 << 24)) return SP24_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return SP24_OK;
   const int64_t cols = act == SP24_ACT_SWIGLU ? N / 2 : N;
   const int yb = elem_bytes(y_dtype);
@@ -123,7 +123,7 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   if (!x || !w->codes || !w->scales) return SP24_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 4) || !aligned(w->zeros, 4)) return SP24_ERR_ALIGN;
   const GemvW4 p{x, w->codes, reinterpret_cast<const uint16_t*>(w->scales), w->zeros, grouped ? offsets : nullptr, y,
-                 M, E, N, K, w->scale_dtype, w->group, act, y_dtype == SP24_F32, 0, 0};
+                 M, E, N, K, w->scale_dtype, w->group, act, y_dtype == SP24_F32, 0};
   return x_dtype == SP24_BF16 ? gemv_w4_bf16(p, s) : gemv_w4_f16(p, s);
 }
 

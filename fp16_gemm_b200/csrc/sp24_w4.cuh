@@ -28,11 +28,10 @@ struct GemvW4 {
   void* y;
   int64_t M, E, N, K;
   int scale_dtype, group, act, y_f32;
-  int wk;      // warps along K (a power of two); the other 8 / wk take further columns
-  int x_rows;  // rows of x that shared memory has room for
+  int wk_log;  // chosen by the launch: log2 of the warps that share an item's K
 };
 
-int gemv_w4_bf16(GemvW4 p, cudaStream_t s);
-int gemv_w4_f16(GemvW4 p, cudaStream_t s);
+int gemv_w4_bf16(const GemvW4& p, cudaStream_t s);
+int gemv_w4_f16(const GemvW4& p, cudaStream_t s);
 
 }  // namespace sp24

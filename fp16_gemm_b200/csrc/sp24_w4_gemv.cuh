@@ -7,9 +7,11 @@ namespace sp24 {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kWarps = 8;
-constexpr int kChunk = 128;     // entries of K per stage: 64 code bytes of each row
+constexpr int kWarps = 16;
+constexpr int kChunk = 256;     // entries of K per stage: 128 code bytes of each row
+constexpr int kWarpsLog = 4;
 constexpr int kTileBytes = 16 * kChunk / 2;
+constexpr int kSmemMax = 232448;  // of one CTA
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -147,38 +149,37 @@ __device__ __forceinline__ TokenTile next_tile(const GemvW4& p, int step, const 
   return t;  // not reached
 }
 
-// Work items are (token tile, column tile) pairs.  A CTA walks a run of them: contiguous with
-// experts (column tiles of one expert follow each other), every gridDim.x-th otherwise (token tiles
-// of one column tile follow each other).
+// Work items are (token tile, column tile) pairs; a team of warps walks a run of them: contiguous with
+// experts (column tiles of one expert follow each other), every `teams`-th otherwise (token tiles of
+// one column tile follow each other).
 template <int STEP>
 struct Walk {
-  int64_t left;       // items still to come, this one included
-  int64_t item;       // without experts
-  int64_t col;        // column tile
+  int left;   // items still to come, this one included
+  int item;   // without experts
+  int col;    // column tile
   TokenTile tok;
 
-  __device__ __forceinline__ void start(const GemvW4& p, int64_t col_tiles) {
-    const int64_t cta = blockIdx.x, ctas = gridDim.x;
+  __device__ __forceinline__ void start(const GemvW4& p, int col_tiles, int team, int teams) {
     if (p.offsets) {
       int64_t mine, upto;
       const int64_t all = count_tiles(p, STEP, mine, upto) * col_tiles;
-      const int64_t first = all * cta / ctas;
-      left = all * (cta + 1) / ctas - first;
+      const int64_t first = all * team / teams;
+      left = (int)(all * (team + 1) / teams - first);
       if (left <= 0) return;
-      col = first % col_tiles;
+      col = (int)(first % col_tiles);
       tok = find_tile(p, STEP, mine, upto, first / col_tiles);
     } else {
-      const int64_t tiles = (p.M + STEP - 1) / STEP, all = tiles * col_tiles;
-      item = cta;
-      left = all > cta ? (all - cta + ctas - 1) / ctas : 0;
+      const int tiles = (int)((p.M + STEP - 1) / STEP), all = tiles * col_tiles;
+      item = team;
+      left = all > team ? (all - team + teams - 1) / teams : 0;
       place(p, tiles);
     }
   }
-  __device__ __forceinline__ void place(const GemvW4& p, int64_t tiles) {
+  __device__ __forceinline__ void place(const GemvW4& p, int tiles) {
     col = tiles == 1 ? item : item / tiles;
     tok = {0, tiles == 1 ? 0 : (item - col * tiles) * STEP, p.M};
   }
-  __device__ __forceinline__ void advance(const GemvW4& p, int64_t col_tiles) {
+  __device__ __forceinline__ void advance(const GemvW4& p, int col_tiles, int teams) {
     if (--left <= 0) return;
     if (p.offsets) {
       if (++col == col_tiles) {
@@ -186,160 +187,142 @@ struct Walk {
         tok = next_tile(p, STEP, tok);
       }
     } else {
-      item += gridDim.x;
-      place(p, (p.M + STEP - 1) / STEP);
+      item += teams;
+      place(p, (int)((p.M + STEP - 1) / STEP));
     }
   }
   __device__ __forceinline__ int rows() const { return (int)min((int64_t)STEP, tok.m1 - tok.m0); }
 };
 
-// y = x W^T for up to 8 NT rows of x and MT tiles of 16 weight rows per warp (with SwiGLU: a gate
-// tile and its up tile).  The weight rows are the MMA's M, the rows of x its N.
+// y = x W^T for up to 8 NT rows of x and MT tiles of 16 weight rows (with SwiGLU: a gate tile and its
+// up tile).  The weight rows are the MMA's M, the rows of x its N.
 //
-// Persistent: a CTA walks its work items with the loads running S chunks ahead across their borders.
-// K is split over wk warps of the CTA in chunks of 128 entries; each warp streams its chunks of codes
-// through a ring of S stages of its own with cp.async, so within an item no warp waits for another.
-// An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of a 32-entry
-// block of rows g and g + 8; the MMA may sum K in any order, so the pairs that expand8 gives are fed
-// as they come, with x's pairs picked alike.  A group's sum is scaled in fp32; the warps' partial
-// sums meet in shared memory in a fixed order, in two buffers that take turns, so one barrier per
-// item is enough.
+// Persistent, one CTA of 16 warps per SM.  2^wk_log warps are a team, which walks work items of its
+// own: K is split over them in chunks of 256 entries, each warp streaming its chunks of codes and
+// scales through a ring of S stages with cp.async that runs ahead across the items' borders; the
+// partial sums meet in shared memory in a fixed order, in two buffers that take turns, so one barrier
+// of the team per item is enough.  An ldmatrix of 16-byte row pieces hands lane (g, t) the eight
+// codes 8t .. 8t + 7 of a 32-entry block of rows g and g + 8; the MMA may sum K in any order, so the
+// pairs that expand8 gives are fed as they come, with x's pairs picked alike.  A group's sum is
+// scaled in fp32.
 //
-// XW: x stands in shared memory whole, its pairs picked when it is brought there (few rows of x, one
-// matrix); otherwise its chunk travels in the ring and the pairs are picked at each use.
+// XW: x stands in shared memory whole, its pairs picked when it is brought there; otherwise (experts,
+// or a large x) it is read from global memory half a chunk ahead and its pairs are picked at each use.
 template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
 struct GemvKernel {
   static constexpr int kTok = 8 * NT;
-  static constexpr int kCols = SWIGLU ? 16 : 16 * MT;    // output columns per warp
-  static constexpr int kGroups = 4 / GB;                 // groups per chunk
+  static constexpr int kCols = SWIGLU ? 16 : 16 * MT;    // output columns of an item
+  static constexpr int kGroups = kChunk / 32 / GB;       // groups per chunk
   // A chunk's scales of one row are 2 kGroups bytes at any even place, its zero points kGroups bytes
   // at any place: the aligned words that they may touch are copied.
   static constexpr int kScaleWords = kGroups / 2 + 1;
-  static constexpr int kZeroWords = ZEROS ? (kGroups == 1 ? 1 : 2) : 0;
+  static constexpr int kZeroWords = ZEROS ? (kGroups + 2) / 4 + 1 : 0;
   static constexpr int kZeroAt = 16 * MT * kScaleWords * 4;                     // in bytes, behind the scales
-  static constexpr int kScaleBytes = kZeroAt + 16 * MT * kZeroWords * 4;
-  static constexpr int kPartial = kWarps * MT * kTok * 16;       // floats of one buffer
+  static constexpr int kStage = MT * kTileBytes + (kZeroAt + 16 * MT * kZeroWords * 4 + 127) / 128 * 128;
+  static constexpr int kPartial = MT * kTok * 16;                               // floats per warp and buffer
+  static constexpr int kFixed = 2 * kWarps * kPartial * 4 + kWarps * S * kStage;
 
-  static __host__ __device__ __forceinline__ int stage_bytes(int x_rows) {
-    return MT * kTileBytes + kScaleBytes + (XW ? 0 : x_rows * 2 * kChunk);
-  }
   static __host__ __device__ __forceinline__ int x_stride(int K) {
     return (2 * K + 127) / 128 * 128 + 64;  // two neighbouring rows of x never meet in a bank
   }
-  static int64_t smem_bytes(const GemvW4& p) {
-    return 2 * kPartial * 4 + (int64_t)kWarps * S * stage_bytes(p.x_rows) + (XW ? p.x_rows * x_stride((int)p.K) : 0);
-  }
+  static int64_t smem_bytes(const GemvW4& p) { return kFixed + (XW ? p.M * x_stride((int)p.K) : 0); }
 
   static __device__ __forceinline__ void run(const GemvW4& p, uint8_t* smem) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
     const int g = lane >> 2, t = lane & 3;
-    const int wk = p.wk, wn = kWarps / wk;
-    const int kw = warp & (wk - 1), nw = warp / wk;
+    const int wk = 1 << p.wk_log, kw = warp & (wk - 1), in_cta = warp >> p.wk_log;
+    const int team = in_cta * gridDim.x + blockIdx.x, teams = gridDim.x << (kWarpsLog - p.wk_log);
     const int64_t cols = SWIGLU ? p.N / 2 : p.N;
-    const int64_t col_tiles = (cols + kCols * wn - 1) / (kCols * wn);
+    const int col_tiles = (int)((cols + kCols - 1) / kCols);
     const int K = (int)p.K, KG = K / (32 * GB);
     const int chunks = (K + kChunk - 1) / kChunk;
 
-    const int stage_size = stage_bytes(p.x_rows);
-    float* partial = reinterpret_cast<float*>(smem);
-    uint8_t* ring = smem + 2 * kPartial * 4 + warp * S * stage_size;
-    uint8_t* x_all = smem + 2 * kPartial * 4 + kWarps * S * stage_size;
+    float* const partials = reinterpret_cast<float*>(smem);  // [buffer][warp][tile][token][row]
+    uint8_t* const ring = smem + 2 * kWarps * kPartial * 4 + warp * S * kStage;
+    uint8_t* const x_all = smem + kFixed;
     const uint32_t ring_at = smem_addr(ring);
 
     Walk<kTok> load, use;  // what is being fetched and what is being multiplied
-    load.start(p, col_tiles);
-    if (load.left <= 0) return;
+    load.left = 0;
+    if (team < teams) load.start(p, col_tiles, team, teams);
     use = load;
 
-    // ---- fetching: chunk load_c of the item `load`
+    // ---- fetching: chunk load_c of the item `load`.  Lane l copies piece l & 7 of rows (l >> 3) + 4 h.
     int load_c = kw;
-    const uint8_t* code_src[MT][2];
-    const uint8_t* x_src = nullptr;
+    const uint8_t* code_src[MT][4];
     const int64_t groups_total = p.E * p.N * KG;
-    int64_t row_group[(16 * MT * kScaleWords + 31) / 32];  // first group of the rows whose words this lane copies
-    int64_t row_group_z[(16 * MT * (ZEROS ? kZeroWords : 1) + 31) / 32];
-    int load_rows = 0;
+    constexpr int kScaleOps = (16 * MT * kScaleWords + 31) / 32, kZeroOps = (16 * MT * kZeroWords + 31) / 32;
+    int64_t scale_group[kScaleOps], zero_group[kZeroOps ? kZeroOps : 1];  // first group of the row a word belongs to
     auto aim = [&]() {  // the sources of a new item
-      const int64_t col0 = (load.col * wn + nw) * kCols;
-      auto weight_row = [&](int i, int r) {  // past the end: the last row, computed and not stored
-        const int64_t c = min(col0 + (SWIGLU ? r : 16 * i + r), cols - 1);
-        return load.tok.e * p.N + (SWIGLU ? i * cols : 0) + c;
+      const int left = (int)min((int64_t)kCols, cols - (int64_t)load.col * kCols);  // columns of this item
+      const int64_t row0 = load.tok.e * p.N + (int64_t)load.col * kCols;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        // rows past the end repeat the last one; they are computed and not stored
+        const int64_t base = row0 + (SWIGLU ? i * cols : 0);
+        const uint8_t* const src = p.codes + base * (K / 2) + (16 * (lane & 7) + kw * (kChunk / 2));
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          code_src[i][h] = src + (int64_t)min((SWIGLU ? 0 : 16 * i) + (lane >> 3) + 4 * h, left - 1) * (K / 2);
+      }
+      auto first_group = [&](int r) {
+        return (row0 + (SWIGLU ? (r >> 4) * cols : 0) + min(SWIGLU ? r & 15 : r, left - 1)) * KG + kw * kGroups;
       };
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < kScaleOps; ++i) scale_group[i] = first_group((lane + 32 * i) / kScaleWords & (16 * MT - 1));
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          code_src[i][h] = p.codes + weight_row(i, g + 8 * h) * (p.K / 2) + 16 * t + kw * (kChunk / 2);
-#pragma unroll
-      for (int i = 0; 32 * i < 16 * MT * kScaleWords; ++i) {
-        const int r = (lane + 32 * i) / kScaleWords;
-        row_group[i] = weight_row(r >> 4 & (MT - 1), r & 15) * KG + kw * kGroups;
-      }
-#pragma unroll
-      for (int i = 0; 32 * i < 16 * MT * kZeroWords; ++i) {
-        const int r = (lane + 32 * i) / (ZEROS ? kZeroWords : 1);
-        row_group_z[i] = weight_row(r >> 4 & (MT - 1), r & 15) * KG + kw * kGroups;
-      }
-      if (!XW) {
-        x_src = reinterpret_cast<const uint8_t*>(p.x) + load.tok.m0 * p.K * 2;
-        load_rows = load.rows();
-      }
+      for (int i = 0; i < kZeroOps; ++i)
+        zero_group[i] = first_group((lane + 32 * i) / (ZEROS ? kZeroWords : 1) & (16 * MT - 1));
     };
-    const uint32_t code_dst = ring_at + g * 64 + 16 * (t ^ (g >> 1 & 3));  // rows g and g + 8 swizzle alike
+    // rows r, r + 8 swizzle alike; a row's pieces (16 bytes) change places by its number
+    const uint32_t code_dst = ring_at + (lane >> 3) * 128;
     auto fetch = [&](int slot) {
       if (load.left > 0) {
-        const int k0 = load_c * kChunk;
-        const uint32_t dst = code_dst + slot * stage_size;
-        if (k0 + 32 * t < K) {
+        const uint32_t dst = code_dst + slot * kStage;
+        if (load_c * kChunk + 32 * (lane & 7) < K) {
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) copy16(dst + i * kTileBytes + h * 512, code_src[i][h]);
+            for (int h = 0; h < 4; ++h)
+              copy16(dst + i * kTileBytes + h * 512 + 16 * ((lane & 7) ^ ((lane >> 3) + 4 * (h & 1))), code_src[i][h]);
         }
-        const uint32_t table = ring_at + slot * stage_size + MT * kTileBytes;
+        const uint32_t table = ring_at + slot * kStage + MT * kTileBytes;
 #pragma unroll
-        for (int i = 0; 32 * i < 16 * MT * kScaleWords; ++i) {
+        for (int i = 0; i < kScaleOps; ++i) {
           const int s = lane + 32 * i, w = s % kScaleWords;
-          const int64_t at = row_group[i];
-          if (s < 16 * MT * kScaleWords && 2 * w < (at & 1) + kGroups)
+          const int64_t at = scale_group[i];
+          if (s < 16 * MT * kScaleWords && 2 * w < ((int)at & 1) + kGroups)
             copy4(table + 4 * s, p.scales, (at >> 1) * 4 + 4 * w, 2 * groups_total);
-          row_group[i] += wk * kGroups;
+          scale_group[i] += wk * kGroups;
         }
 #pragma unroll
-        for (int i = 0; 32 * i < 16 * MT * kZeroWords; ++i) {
+        for (int i = 0; i < kZeroOps; ++i) {
           const int s = lane + 32 * i, w = s % (ZEROS ? kZeroWords : 1);
-          const int64_t at = row_group_z[i];
-          if (s < 16 * MT * kZeroWords && 4 * w < (at & 3) + kGroups)
+          const int64_t at = zero_group[i];
+          if (s < 16 * MT * kZeroWords && 4 * w < ((int)at & 3) + kGroups)
             copy4(table + kZeroAt + 4 * s, p.zeros, (at >> 2) * 4 + 4 * w, groups_total);
-          row_group_z[i] += wk * kGroups;
-        }
-        if (!XW) {  // x: row m's 256 bytes at 256 m, its 16-byte piece j at 16 (j ^ 4 (m & 1))
-          const uint32_t xdst = ring_at + slot * stage_size + MT * kTileBytes + kScaleBytes;
-          for (int j = lane; j < load_rows * 16; j += 32) {
-            const int m = j >> 4, piece = j & 15;
-            if (k0 + 8 * piece < K)
-              copy16(xdst + m * 256 + 16 * (piece ^ (m & 1) * 4), x_src + ((int64_t)m * K + k0 + 8 * piece) * 2);
-          }
+          zero_group[i] += wk * kGroups;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) code_src[i][h] += wk * (kChunk / 2);
+          for (int h = 0; h < 4; ++h) code_src[i][h] += wk * (kChunk / 2);
         load_c += wk;
         if (load_c >= chunks) {
-          load.advance(p, col_tiles);
+          load.advance(p, col_tiles, teams);
           load_c = kw;
           if (load.left > 0) aim();
         }
       }
       copy_commit();
     };
-    aim();
+
+    if (load.left > 0) aim();
 #pragma unroll
     for (int s = 0; s < S; ++s) fetch(s);
     if (XW) {
-      const int pieces = K / 8, rows = (int)p.M;
-      for (int m = 0; m < rows; ++m)
+      const int pieces = K / 8;
+      for (int m = 0; m < (int)p.M; ++m)
         for (int j = threadIdx.x; j < pieces; j += 32 * kWarps) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)m * pieces + j);
           *reinterpret_cast<uint4*>(x_all + m * x_stride(K) + 16 * j) =
@@ -348,6 +331,7 @@ struct GemvKernel {
         }
       __syncthreads();
     }
+    if (use.left <= 0) return;
 
     // ---- multiplying
     float tot[MT][NT][4], acc[MT][NT][4];
@@ -356,98 +340,115 @@ struct GemvKernel {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tot[i][n][k] = acc[i][n][k] = 0.0f;
+        for (int k = 0; k < 4; ++k) tot[i][n][k] = 0.0f;
 
     // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4)
     const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
-    const uint32_t lm_at = ring_at + lm_row * 64;
-    const int lm_sw = lm_row >> 1 & 3, lm_block = lane >> 4;
+    const uint32_t lm_at = ring_at + lm_row * 128;
     const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
-    int x_flip[NT];
-    int group_row[MT];  // (this lane's row of tile i) * KG, as far as its place within a word goes
+    int group_row[MT];         // (this lane's row of tile i) * KG, as far as its place within a word goes
     auto aim_use = [&]() {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int64_t row = use.tok.e * p.N + (SWIGLU ? i * cols : 16 * i) + (use.col * wn + nw) * kCols + g;
+        const int64_t row = use.tok.e * p.N + (SWIGLU ? i * cols : 16 * i) + (int64_t)use.col * kCols + g;
         group_row[i] = (int)(row & 3) * KG;
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int m = min(8 * n + g, use.rows() - 1);
-        x_row[n] = XW ? x_all + m * x_stride(K) + 16 * t : ring + MT * kTileBytes + kScaleBytes + m * 256 + 16 * t;
-        x_flip[n] = (m & 1) * 64;
+        x_row[n] = XW ? x_all + m * x_stride(K) + 16 * t
+                      : reinterpret_cast<const uint8_t*>(p.x) + ((use.tok.m0 + m) * K + 8 * t) * 2;
       }
     };
     aim_use();
 
-    int slot = 0, c = kw;
-    while (true) {
-      copy_wait<S - 1>();
-      __syncwarp();
-      const int blocks = min(4, K / 32 - 4 * c);
-      const uint8_t* table = ring + slot * stage_size + MT * kTileBytes;
+    uint4 xv[NT][4];
+    // x of blocks 4 half .. 4 half + 3 of chunk c, as it stands in memory
+    auto read_x = [&](int c, int half, int blocks) {
 #pragma unroll
-      for (int jj = 0; jj < 4; jj += 2) {
-        if (jj >= blocks) break;
-        uint32_t words[MT][4];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          ldmatrix4(words[i], lm_at + slot * stage_size + i * kTileBytes + 16 * ((jj + lm_block) ^ lm_sw));
+        for (int j = 0; j < 4; ++j)
+          if (4 * half + j < blocks)
+            xv[n][j] = XW ? *reinterpret_cast<const uint4*>(x_row[n] + c * (2 * kChunk) + 64 * (4 * half + j))
+                          : __ldg(reinterpret_cast<const uint4*>(x_row[n] + (int64_t)c * (2 * kChunk) + 64 * (4 * half + j)));
+    };
+    // blocks j, j + 1 of the chunk
+    auto multiply2 = [&](int slot, int c, int j, const uint4 (&x0)[NT], const uint4 (&x1)[NT], bool both) {
+      const uint8_t* const table = ring + slot * kStage + MT * kTileBytes;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        uint32_t words[4];
+        ldmatrix4(words, lm_at + slot * kStage + i * kTileBytes + 16 * ((j + (lane >> 4)) ^ (lane & 7)));
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
-          const int j = jj + jb;
-          if (j >= blocks) break;
-          uint32_t b[NT][4];
+          if (jb && !both) break;
+          const int jj = j + jb;
+          uint32_t zl = kMagic<XT> + 0x80008u, zh = zl;
+          const int first = group_row[i] + c * kGroups;  // rows g and g + 8 start alike within a word
+          if (ZEROS) {
+            const uint8_t* zp = table + kZeroAt + (16 * i + g) * kZeroWords * 4 + (first & 3) + jj / GB;
+            zl = kMagic<XT> + (zp[0] & 15u) * 0x10001u;
+            zh = kMagic<XT> + (zp[8 * kZeroWords * 4] & 15u) * 0x10001u;
+          }
+          uint32_t lo[4], hi[4];
+          expand8<XT>(words[2 * jb], zl, lo);
+          expand8<XT>(words[2 * jb + 1], zh, hi);
+          const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            if (XW) {
-              const uint4 v = *reinterpret_cast<const uint4*>(x_row[n] + c * 256 + 64 * j);
-              b[n][0] = v.x, b[n][1] = v.y, b[n][2] = v.z, b[n][3] = v.w;
-            } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(x_row[n] + slot * stage_size + (64 * j ^ x_flip[n]));
-              b[n][0] = __byte_perm(v.x, v.z, 0x5410);
-              b[n][1] = __byte_perm(v.x, v.z, 0x7632);
-              b[n][2] = __byte_perm(v.y, v.w, 0x5410);
-              b[n][3] = __byte_perm(v.y, v.w, 0x7632);
+            uint4 b = jb ? x1[n] : x0[n];
+            if (!XW)
+              b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
+                             __byte_perm(b.y, b.w, 0x7632));
+            if (jj % GB == 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[i][n][k] = 0.0f;
             }
+            mma16816<XT>(acc[i][n], a0, b.x, b.y);
+            mma16816<XT>(acc[i][n], a1, b.z, b.w);
           }
+          if ((jj + 1) % GB == 0) {
+            const uint8_t* sp = table + (16 * i + g) * kScaleWords * 4 + 2 * ((first & 1) + jj / GB);
+            const uint32_t l = *reinterpret_cast<const uint16_t*>(sp);
+            const uint32_t h = *reinterpret_cast<const uint16_t*>(sp + 8 * kScaleWords * 4);
+            const float sl = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(l) : W4Half<SP24_F16>::get(l);
+            const float sh = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(h) : W4Half<SP24_F16>::get(h);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            float sl, sh;
-            uint32_t zl = kMagic<XT> + 0x80008u, zh = zl;
-            {
-              // rows g and g + 8 start alike within a word: 8 KG is a multiple of 4
-              const int first = group_row[i] + c * kGroups;
-              const uint8_t* sp = table + (16 * i + g) * kScaleWords * 4 + 2 * ((first & 1) + j / GB);
-              const uint32_t l = *reinterpret_cast<const uint16_t*>(sp);
-              const uint32_t h = *reinterpret_cast<const uint16_t*>(sp + 8 * kScaleWords * 4);
-              sl = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(l) : W4Half<SP24_F16>::get(l);
-              sh = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(h) : W4Half<SP24_F16>::get(h);
-              if (ZEROS) {
-                const uint8_t* zp = table + kZeroAt + (16 * i + g) * kZeroWords * 4 + (first & 3) + j / GB;
-                zl = kMagic<XT> + (zp[0] & 15u) * 0x10001u;
-                zh = kMagic<XT> + (zp[8 * kZeroWords * 4] & 15u) * 0x10001u;
-              }
-            }
-            uint32_t lo[4], hi[4];
-            expand8<XT>(words[i][2 * jb], zl, lo);
-            expand8<XT>(words[i][2 * jb + 1], zh, hi);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t a[4] = {lo[2 * half], hi[2 * half], lo[2 * half + 1], hi[2 * half + 1]};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<XT>(acc[i][n], a, b[n][2 * half], b[n][2 * half + 1]);
-            }
-            if ((j + 1) % GB == 0) {
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  tot[i][n][k] = fmaf(k < 2 ? sl : sh, acc[i][n][k], tot[i][n][k]);
-                  acc[i][n][k] = 0.0f;
-                }
-            }
+              for (int k = 0; k < 4; ++k) tot[i][n][k] = fmaf(k < 2 ? sl : sh, acc[i][n][k], tot[i][n][k]);
           }
+        }
+      }
+    };
+    auto multiply = [&](int slot, int c, int half, int blocks) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint4 x0[NT], x1[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x0[n] = xv[n][j], x1[n] = xv[n][j + 1];
+        if (4 * half + j < blocks) multiply2(slot, c, 4 * half + j, x0, x1, 4 * half + j + 1 < blocks);
+      }
+    };
+
+    int slot = 0, c = kw, buffer = 0;
+    while (true) {
+      const int blocks = min(kChunk / 32, K / 32 - kChunk / 32 * c);
+      if (blocks == kChunk / 32) {  // a whole chunk: straight through
+        read_x(c, 0, kChunk / 32);
+        copy_wait<S - 1>();
+        __syncwarp();
+        multiply(slot, c, 0, kChunk / 32);
+        read_x(c, 1, kChunk / 32);
+        multiply(slot, c, 1, kChunk / 32);
+      } else {
+        copy_wait<S - 1>();
+        __syncwarp();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          read_x(c, half, blocks);
+          multiply(slot, c, half, blocks);
         }
       }
       __syncwarp();
@@ -456,8 +457,9 @@ struct GemvKernel {
       c += wk;
       if (c < chunks) continue;
 
-      // ---- the item is done: partial[warp][tile][token][row]
+      // ---- the item is done
       const int rows = use.rows();
+      float* const mine = partials + (buffer * kWarps + warp) * kPartial;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -465,20 +467,23 @@ struct GemvKernel {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int m = 8 * n + 2 * t + (k & 1);
-            if (m < rows) partial[((warp * MT + i) * kTok + m) * 16 + g + 8 * (k >> 1)] = tot[i][n][k];
+            if (m < rows) mine[(i * kTok + m) * 16 + g + 8 * (k >> 1)] = tot[i][n][k];
             tot[i][n][k] = 0.0f;
           }
-      __syncthreads();
+      if (wk == 1)
+        __syncwarp();
+      else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + in_cta), "r"(32 * wk) : "memory");
+      const float* const team_sums = partials + (buffer * kWarps + (in_cta << p.wk_log)) * kPartial;
       constexpr int kOutTiles = SWIGLU ? 1 : MT;
-      for (int o = threadIdx.x; o < rows * wn * kOutTiles * 16; o += 32 * kWarps) {
-        const int r = o & 15, m = (o >> 4) / (kOutTiles * wn), tile = (o >> 4) - m * (kOutTiles * wn);
-        const int i = tile & (kOutTiles - 1), w = tile / kOutTiles;
-        const int64_t col = use.col * (kCols * wn) + tile * 16 + r;
+      for (int o = kw * 32 + lane; o < rows * kOutTiles * 16; o += 32 * wk) {
+        const int r = o & 15, i = (o >> 4) % kOutTiles, m = (o >> 4) / kOutTiles;
+        const int64_t col = (int64_t)use.col * kCols + 16 * i + r;
         if (col >= cols) continue;
         float v = 0.0f, up = 0.0f;
         for (int k = 0; k < wk; ++k) {
-          v += partial[(((w * wk + k) * MT + i) * kTok + m) * 16 + r];
-          if (SWIGLU) up += partial[(((w * wk + k) * MT + 1) * kTok + m) * 16 + r];
+          v += team_sums[k * kPartial + (i * kTok + m) * 16 + r];
+          if (SWIGLU) up += team_sums[k * kPartial + (kTok + m) * 16 + r];
         }
         if (SWIGLU) v = v / (1.0f + expf(-v)) * up;
         const int64_t at = (use.tok.m0 + m) * cols + col;
@@ -487,9 +492,9 @@ struct GemvKernel {
         else
           reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)W4Half<XT>::put(v);
       }
-      partial = partial == reinterpret_cast<float*>(smem) ? partial + kPartial : reinterpret_cast<float*>(smem);
+      buffer ^= 1;
       c = kw;
-      use.advance(p, col_tiles);
+      use.advance(p, col_tiles, teams);
       if (use.left <= 0) break;
       aim_use();
     }
@@ -498,35 +503,38 @@ struct GemvKernel {
 };
 
 template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
-__global__ void __launch_bounds__(32 * kWarps, 2) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
+__global__ void __launch_bounds__(32 * kWarps, 1) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
   extern __shared__ __align__(128) uint8_t smem[];
   GemvKernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>::run(p, smem);
 }
 
 template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
-int launch_gemv(const GemvW4& p, cudaStream_t s) {
+int launch_gemv(GemvW4 p, cudaStream_t s) {
   using Kern = GemvKernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>;
   auto kernel = gemv_w4_kernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>;
-  const int64_t bytes = Kern::smem_bytes(p);
-  // what one SM holds of this kernel: the register limit is asked for once per device
-  static int by_regs[64];
+  static bool raised[64];  // the attribute holds per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SP24_ERR_CUDA;
-  if (!by_regs[dev]) {
-    cudaFuncAttributes a;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
-        cudaFuncGetAttributes(&a, kernel) != cudaSuccess)
+  if (!raised[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
       return SP24_ERR_CUDA;
-    by_regs[dev] = 65536 / ((a.numRegs + 7) / 8 * 8 * 32 * kWarps);
+    raised[dev] = true;
   }
-  const int64_t by_smem = 233472 / (bytes + 1024);
-  const int64_t per_sm = by_smem < by_regs[dev] ? by_smem : by_regs[dev];
-  const int64_t cols = SWIGLU ? p.N / 2 : p.N, per_cta = (int64_t)Kern::kCols * (kWarps / p.wk);
-  const int64_t col_tiles = (cols + per_cta - 1) / per_cta;
+  const int64_t cols = SWIGLU ? p.N / 2 : p.N, col_tiles = (cols + Kern::kCols - 1) / Kern::kCols;
   // with experts: the sum of ceil(rows / kTok) is at most this
   const int64_t tok_tiles = (p.M + Kern::kTok - 1) / Kern::kTok + (p.offsets ? (p.E < p.M ? p.E : p.M) : 0);
-  const int64_t room = (per_sm < 1 ? 1 : per_sm) * sm_count(), items = col_tiles * tok_tiles;
-  kernel<<<(unsigned)(items < room ? items : room), 32 * kWarps, (size_t)bytes, s>>>(p);
+  const int64_t items = col_tiles * tok_tiles, chunks = (p.K + kChunk - 1) / kChunk;
+  if (items > INT32_MAX / 2) return SP24_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  // Team size: the fewest rounds of (chunks per warp + about one chunk's time of joining an item).
+  int64_t best = INT64_MAX;
+  for (int k = 0; k <= kWarpsLog && (k == 0 || (1 << k) <= chunks); ++k) {
+    const int64_t teams = (int64_t)sms << (kWarpsLog - k), rounds = (items + teams - 1) / teams;
+    const int64_t cost = rounds * ((chunks + (1 << k) - 1) >> k) * 2 + rounds;
+    if (cost < best) best = cost, p.wk_log = k;
+  }
+  const int64_t ctas = items < sms ? items : sms;
+  kernel<<<(unsigned)ctas, 32 * kWarps, (size_t)Kern::smem_bytes(p), s>>>(p);
   return launch_status();
 }
 
@@ -543,20 +551,21 @@ int by_group(const GemvW4& p, cudaStream_t s) {
 }
 
 template <int XT>
-int gemv_by_shape(GemvW4 p, cudaStream_t s) {
-  const int64_t chunks = (p.K + kChunk - 1) / kChunk;
-  p.wk = chunks >= 8 ? 8 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+int gemv_by_shape(const GemvW4& p, cudaStream_t s) {
   // sixteen rows of x per tile only where eight would leave a second tile per matrix
   const bool wide = p.M > 8 * p.E;
-  const int tok = wide ? 16 : 8;
-  p.x_rows = (int)(p.M < tok ? p.M : tok);
-  const bool whole = !p.offsets && p.x_rows * p.K <= 16384;  // at most 32 KB of shared memory for x
+  const int64_t x_bytes = p.M * ((2 * p.K + 127) / 128 * 128 + 64);
+  const bool one = !p.offsets && p.M <= 16;  // one tile of x for the whole matrix
   if (p.act == SP24_ACT_SWIGLU) {
-    if (wide) return by_group<XT, 2, 2, 2, true, false>(p, s);
-    return whole ? by_group<XT, 1, 2, 3, true, true>(p, s) : by_group<XT, 1, 2, 2, true, false>(p, s);
+    if (one && !wide && x_bytes <= kSmemMax - GemvKernel<XT, 1, 2, 2, true, true, true, 1>::kFixed)
+      return by_group<XT, 1, 2, 2, true, true>(p, s);
+    return wide ? by_group<XT, 2, 2, 2, true, false>(p, s) : by_group<XT, 1, 2, 2, true, false>(p, s);
   }
-  if (wide) return by_group<XT, 2, 2, 2, false, false>(p, s);
-  return whole ? by_group<XT, 1, 1, 6, false, true>(p, s) : by_group<XT, 1, 2, 2, false, false>(p, s);
+  if (one && !wide && x_bytes <= kSmemMax - GemvKernel<XT, 1, 1, 3, false, true, true, 1>::kFixed)
+    return by_group<XT, 1, 1, 3, false, true>(p, s);
+  if (one && wide && x_bytes <= kSmemMax - GemvKernel<XT, 2, 1, 2, false, true, true, 1>::kFixed)
+    return by_group<XT, 2, 1, 2, false, true>(p, s);
+  return wide ? by_group<XT, 2, 2, 2, false, false>(p, s) : by_group<XT, 1, 2, 2, false, false>(p, s);
 }
 
 }  // namespace

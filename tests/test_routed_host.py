@@ -88,7 +88,7 @@ def test_gemv_w4_refusals(grouped):
         return _raw("sp24_gemv_w4", x, dt, ctypes.byref(op), M, N, K, act, y, ydt, None)
     assert f(dt=sp.F32) == f(ydt=sp.F16) == f(ydt=sp.NVFP4) == f(_op(scale=sp.F32)) == sp.ERR_DTYPE
     assert f(act=2) == f(x=None) == f(y=None) == f(_op(codes=None)) == f(_op(scales=None)) == sp.ERR_INVALID_ARG
-    assert f(_op(group=96)) == f(K=2**30) == f(M=2**31) == f(N=2**31) == sp.ERR_UNSUPPORTED
+    assert f(_op(group=96)) == f(K=2**24 + 128) == f(M=2**31) == f(N=2**31) == sp.ERR_UNSUPPORTED
     assert f(K=192) == f(K=-128) == f(M=-1) == f(N=-1) == f(N=5, act=1) == sp.ERR_SHAPE
     assert f(x=24) == f(y=18) == f(_op(codes=24)) == f(_op(scales=18)) == f(_op(zeros=18)) == sp.ERR_ALIGN
     assert f(M=0, x=None, y=None) == f(N=0, y=None) == sp.OK

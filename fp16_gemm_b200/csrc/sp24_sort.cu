@@ -11,6 +11,7 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 8;
 constexpr int kMaxUnsortTopk = 64;
+constexpr int kCounters = 8192;  // counters of one pass over a chunk (32 KB of shared memory)
 
 // ------------------------------------------------------------------ element access
 
@@ -42,51 +43,127 @@ struct alignas(sizeof(T) * V) Vec {
 };
 
 // ------------------------------------------------------------------ sort
+//
+// The row of entry i is the number of entries before it in the order (expert, entry number).  One
+// warp finds it by counting and then moves the entry's row of x.
+//
+// Few entries: every warp counts over all of them, in one launch.  Many: the entries are cut into
+// chunks of 2^chunk_log; a first launch counts each chunk's entries per expert (and all of them, by
+// integer atomics, whose order does not matter), and the warp adds up the totals of lower experts, its
+// expert's counts in earlier chunks and the equal entries before it in its own chunk.  Its reads grow
+// like E + n / chunk + chunk instead of n, so the chunk is about sqrt(n).
 
-// One warp per entry (then one per offset): the row of entry i is the number of entries that come
-// before it, counted over all of them.
-template <int BYTES>
-__global__ void __launch_bounds__(32 * kWarps) sort_count_kernel(const uint8_t* __restrict__ x,
-                                                                 const int32_t* __restrict__ routing, int64_t n,
-                                                                 int topk, int64_t E, int64_t row_bytes,
-                                                                 uint8_t* __restrict__ xs, int32_t* __restrict__ pos,
-                                                                 int32_t* __restrict__ src,
-                                                                 int32_t* __restrict__ row_expert,
-                                                                 int32_t* __restrict__ offsets) {
+struct SortTables {
+  const int32_t* routing;
+  int64_t n, E;
+  int32_t *pos, *src, *row_expert, *offsets;
+  const int32_t* counts;  // [E + 1][chunks]: by expert (E: the empty slots), then by chunk
+  const int32_t* totals;  // [E + 1]
+  int64_t chunks;
+  int chunk_log;
+};
+
+// The expert of an entry; empty slots come after every expert.
+__device__ __forceinline__ int64_t entry_key(int32_t id, int64_t E) { return id < 0 || id >= E ? E : id; }
+
+template <bool MANY>
+__device__ __forceinline__ int entries_below(const SortTables& t, int64_t key) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  if (MANY) {
+    for (int64_t e = lane; e < key; e += 32) before += t.totals[e];
+  } else {
+    for (int64_t j = lane; j < t.n; j += 32) before += entry_key(t.routing[j], t.E) < key;
+  }
+  return before;
+}
+
+template <bool MANY>
+__device__ __forceinline__ int equal_before(const SortTables& t, int64_t key, int64_t i) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  int64_t from = 0;
+  if (MANY) {
+    const int64_t chunk = i >> t.chunk_log;
+    const int32_t* const mine = t.counts + key * t.chunks;
+    for (int64_t c = lane; c < chunk; c += 32) before += mine[c];
+    from = chunk << t.chunk_log;
+  }
+  for (int64_t j = from + lane; j < i; j += 32) before += entry_key(t.routing[j], t.E) == key;
+  return before;
+}
+
+// One warp per entry, then one per offset.
+template <int BYTES, bool MANY>
+__global__ void __launch_bounds__(32 * kWarps) sort_kernel(const __grid_constant__ SortTables t,
+                                                           const uint8_t* __restrict__ x, int topk, int64_t row_bytes,
+                                                           uint8_t* __restrict__ xs) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= n + E + 1) return;
-  const bool entry = i < n;
-  int64_t key = i - n;  // an offset counts the entries of lower experts
-  if (entry) {
-    key = routing[i];
-    if (key < 0 || key >= E) {
-      if (key != -1 && lane == 0) set_dev_error(SP24_ERR_INVALID_ARG);
-      key = E;  // empty slots come after every expert
-    }
-  }
-  int before = 0;
-  for (int64_t j = lane; j < n; j += 32) {
-    int64_t k = routing[j];
-    if (k < 0 || k >= E) k = E;
-    before += k < key || (entry && k == key && j < i);
-  }
-  before = __reduce_add_sync(kFull, before);
-  if (!entry) {
-    if (lane == 0) offsets[key] = before;
+  if (i >= t.n + t.E + 1) return;
+  if (i >= t.n) {
+    const int at = __reduce_add_sync(kFull, entries_below<MANY>(t, i - t.n));
+    if (lane == 0) t.offsets[i - t.n] = at;
     return;
   }
-  const bool held = key < E;
+  const int32_t id = t.routing[i];
+  const int64_t key = entry_key(id, t.E);
+  const bool held = key < t.E;
+  if (!held && id != -1 && lane == 0) set_dev_error(SP24_ERR_INVALID_ARG);
+  const int row = __reduce_add_sync(kFull, entries_below<MANY>(t, key) + equal_before<MANY>(t, key, i));
   if (lane == 0) {
-    pos[i] = held ? before : -1;
-    src[before] = held ? (int32_t)i : -1;
-    row_expert[before] = held ? (int32_t)key : -1;
+    t.pos[i] = held ? row : -1;
+    t.src[row] = held ? (int32_t)i : -1;
+    t.row_expert[row] = held ? id : -1;
   }
   if (!held || !x) return;
   using V = Vec<uint8_t, BYTES>;
   const V* from = reinterpret_cast<const V*>(x + (i / topk) * row_bytes);
-  V* to = reinterpret_cast<V*>(xs + (int64_t)before * row_bytes);
+  V* to = reinterpret_cast<V*>(xs + (int64_t)row * row_bytes);
   for (int64_t c = lane; c < row_bytes / BYTES; c += 32) to[c] = from[c];
+}
+
+// Each CTA counts one chunk; with E + 1 counters in shared memory.
+__global__ void __launch_bounds__(256) sort_count_kernel(const int32_t* __restrict__ routing, int64_t n, int64_t E,
+                                                         int chunk_log, int64_t chunks, int32_t* __restrict__ counts,
+                                                         int32_t* __restrict__ totals) {
+  extern __shared__ int32_t held[];
+  const int64_t from = (int64_t)blockIdx.x << chunk_log, to = min(n, from + ((int64_t)1 << chunk_log));
+  for (int64_t e0 = 0; e0 <= E; e0 += kCounters) {
+    const int span = (int)min((int64_t)kCounters, E + 1 - e0);
+    for (int e = threadIdx.x; e < span; e += 256) held[e] = 0;
+    __syncthreads();
+    for (int64_t j = from + threadIdx.x; j < to; j += 256) {
+      const int64_t key = entry_key(routing[j], E) - e0;
+      if (key >= 0 && key < span) atomicAdd(&held[key], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < span; e += 256) {
+      const int32_t v = held[e];
+      counts[(e0 + e) * chunks + blockIdx.x] = v;
+      if (v) atomicAdd(&totals[e0 + e], v);
+    }
+    __syncthreads();
+  }
+}
+
+// Above this many entries the chunked form is used: see sp24_moe_sort.
+constexpr int64_t kFew = 2048;
+
+struct SortWs {
+  int chunk_log;
+  int64_t chunks, totals_at, counts_at, bytes;
+};
+
+SortWs sort_layout(int64_t n, int64_t E) {
+  SortWs w{};
+  if (n <= kFew) return w;
+  w.chunk_log = 8;
+  while ((1ll << (2 * w.chunk_log)) < n) ++w.chunk_log;
+  w.chunks = (n + (1ll << w.chunk_log) - 1) >> w.chunk_log;
+  w.counts_at = ((E + 1) * 4 + 15) / 16 * 16;
+  w.bytes = w.counts_at + (E + 1) * w.chunks * 4;
+  return w;
 }
 
 // ------------------------------------------------------------------ unsort
@@ -215,7 +292,8 @@ using namespace sp24;
 extern "C" int sp24_moe_sort_workspace_size(int64_t T, int topk, int64_t E, int64_t* bytes) {
   if (!bytes) return SP24_ERR_INVALID_ARG;
   if (T < 0 || topk < 1 || E < 1) return SP24_ERR_SHAPE;
-  *bytes = 0;
+  if (E > (1 << 20) || T > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
+  *bytes = sort_layout(T * topk, E).bytes;
   return SP24_OK;
 }
 
@@ -232,16 +310,33 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   if (!aligned(x, eb) || !aligned(xs, eb) || !aligned(routing, 4) || !aligned(pos, 4) || !aligned(src, 4) ||
       !aligned(row_expert, 4) || !aligned(offsets, 4))
     return SP24_ERR_ALIGN;
-  (void)workspace;
-  (void)workspace_bytes;
+  const SortWs ws = sort_layout(n, E);
+  if (ws.bytes && (!workspace || workspace_bytes < ws.bytes)) return SP24_ERR_WORKSPACE;
+  if (ws.bytes && !aligned(workspace, 16)) return SP24_ERR_ALIGN;
   cudaStream_t s = as_stream(stream);
-  const int64_t warps = n + E + 1, row = H * eb;
-  const unsigned ctas = (unsigned)((warps + kWarps - 1) / kWarps);
+  SortTables t{routing, n, E, pos, src, row_expert, offsets, nullptr, nullptr, ws.chunks, ws.chunk_log};
+  if (ws.bytes) {
+    int32_t* totals = reinterpret_cast<int32_t*>(workspace);
+    int32_t* counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) + ws.counts_at);
+    if (cudaMemsetAsync(totals, 0, (size_t)(E + 1) * 4, s) != cudaSuccess) return SP24_ERR_CUDA;
+    const int64_t counters = E + 1 < kCounters ? E + 1 : kCounters;
+    sort_count_kernel<<<(unsigned)ws.chunks, 256, (size_t)counters * 4, s>>>(routing, n, E, ws.chunk_log, ws.chunks,
+                                                                             counts, totals);
+    const int st = launch_status();
+    if (st) return st;
+    t.totals = totals;
+    t.counts = counts;
+  }
+  const int64_t row = H * eb;
+  const unsigned ctas = (unsigned)((n + E + 1 + kWarps - 1) / kWarps);
+  const uint8_t* from = H ? reinterpret_cast<const uint8_t*>(x) : nullptr;
+  uint8_t* to = reinterpret_cast<uint8_t*>(xs);
   auto run = [&](auto bytes) {
     constexpr int B = decltype(bytes)::value;
-    sort_count_kernel<B><<<ctas, 32 * kWarps, 0, s>>>(
-        H ? reinterpret_cast<const uint8_t*>(x) : nullptr, routing, n, topk, E, row, reinterpret_cast<uint8_t*>(xs),
-        pos, src, row_expert, offsets);
+    if (ws.bytes)
+      sort_kernel<B, true><<<ctas, 32 * kWarps, 0, s>>>(t, from, topk, row, to);
+    else
+      sort_kernel<B, false><<<ctas, 32 * kWarps, 0, s>>>(t, from, topk, row, to);
     return launch_status();
   };
   if (row % 16 == 0 && aligned(x, 16) && aligned(xs, 16)) return run(std::integral_constant<int, 16>{});

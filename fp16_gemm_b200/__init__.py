@@ -16,6 +16,7 @@ import ctypes
 import functools
 import inspect
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional
 
@@ -138,7 +139,7 @@ def lib() -> ctypes.CDLL:
             L.sp24_prepare_sparse_size.argtypes = [I64, I64, P]
             L.sp24_prepare_sparse.argtypes = [P, I64, I64, P, P]
             L.sp24_sparse48_to_mma.argtypes = [P, P, P, I64, I64, P, P, P, P]
-            W4 = ctypes.POINTER(_W4Operand)
+            W4 = P  # a _W4Operand by reference, or its bytes
             L.sp24_moe_route.argtypes = [P, I, I64, I64, I, I, I, P, P, P]
             L.sp24_moe_route_backward.argtypes = [P, I, P, P, I64, I64, I, I, I, P, P]
             L.sp24_moe_sort_workspace_size.argtypes = [I64, I, I64, P]
@@ -857,34 +858,35 @@ def _placed(impl):
     @functools.wraps(impl)
     def call(*args, stream=None, **kw):
         t = args[0] if args else kw.get(name)
-        t = t.codes if isinstance(t, W4Tensor) else t
+        if type(t) is W4Tensor:
+            t = t.codes
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
-        dev = t.device
-        if stream is None and dev.index == torch.cuda.current_device():
+        if stream is None and t.get_device() == torch.cuda.current_device():
             return impl(*args, **kw)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        with torch.cuda.device(t.device), torch.cuda.stream(stream):
             return impl(*args, **kw)
     return call
 
 
-def _raw_stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+# the current stream of a device, as the runtime's own handle
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _arg(t, name: str, dev: torch.device, shape, *dtypes) -> int:
-    """The address of an argument that has to be contiguous, on `dev`, and of this shape and type."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
+def _arg(t, name: str, dev: int, shape, *dtypes) -> int:
+    """The address of an argument that has to be contiguous, on device `dev`, and of this shape and
+    type."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _check(st: int, fn: str) -> None:
@@ -915,14 +917,14 @@ class MoeSorted(NamedTuple):
 def moe_route(logits: torch.Tensor, topk: int, scoring: int = ROUTE_SOFTMAX, renormalize: bool = True, out=None):
     """(routing int32 [T, topk], router_w fp32 [T, topk]) of router logits [T, E]: the topk largest
     logits (ties to the lower expert) and their softmax or sigmoid weights."""
-    dev = logits.device
+    dev = logits.get_device()
     T, E = _dims(logits, "logits", 2)
     lp = _arg(logits, "logits", dev, logits.shape, *_FLOATS)
     if out is None:
         out = (torch.empty((T, topk), dtype=torch.int32, device=dev),
                torch.empty((T, topk), dtype=torch.float32, device=dev))
     routing, w = out
-    _check(lib().sp24_moe_route(lp, _DT[logits.dtype], T, E, topk, scoring, bool(renormalize),
+    _check((_lib or lib()).sp24_moe_route(lp, _DT[logits.dtype], T, E, topk, scoring, bool(renormalize),
                                 _arg(routing, "routing", dev, (T, topk), torch.int32),
                                 _arg(w, "router_w", dev, (T, topk), torch.float32), _raw_stream(dev)), "sp24_moe_route")
     return routing, w
@@ -932,19 +934,20 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: int = ROUTE_SOFTMAX, ren
 def moe_route_backward(d_router_w: torch.Tensor, logits: torch.Tensor, routing: torch.Tensor,
                        scoring: int = ROUTE_SOFTMAX, renormalize: bool = True, out=None) -> torch.Tensor:
     """The gradient of moe_route's logits (their type, [T, E]) from that of its weights."""
-    dev = logits.device
+    dev = logits.get_device()
     T, E = _dims(logits, "logits", 2)
     topk = _dims(routing, "routing", 2)[1]
     lp = _arg(logits, "logits", dev, logits.shape, *_FLOATS)
     if out is None:
         out = torch.empty_like(logits)
-    _check(lib().sp24_moe_route_backward(lp, _DT[logits.dtype], _arg(routing, "routing", dev, (T, topk), torch.int32),
+    _check((_lib or lib()).sp24_moe_route_backward(lp, _DT[logits.dtype], _arg(routing, "routing", dev, (T, topk), torch.int32),
                                          _arg(d_router_w, "d_router_w", dev, (T, topk), torch.float32), T, E, topk,
                                          scoring, bool(renormalize), _arg(out, "out", dev, (T, E), logits.dtype),
                                          _raw_stream(dev)), "sp24_moe_route_backward")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_sort_workspace_bytes(T: int, topk: int, E: int) -> int:
     n = ctypes.c_int64(0)
     _call("sp24_moe_sort_workspace_size", T, topk, E, ctypes.byref(n))
@@ -952,7 +955,7 @@ def moe_sort_workspace_bytes(T: int, topk: int, E: int) -> int:
 
 
 def _sort(x, routing, E: int, out, workspace) -> MoeSorted:
-    dev = routing.device
+    dev = routing.get_device()
     T, topk = _dims(routing, "routing", 2)
     n = T * topk
     xp = xsp = None
@@ -970,7 +973,7 @@ def _sort(x, routing, E: int, out, workspace) -> MoeSorted:
     if workspace is None and ws:
         workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
     wp, wn = (None, 0) if workspace is None else (_arg(workspace, "workspace", dev, workspace.shape, torch.uint8), workspace.numel())
-    _check(lib().sp24_moe_sort(xp, dt, _arg(routing, "routing", dev, (T, topk), torch.int32), T, topk, E, H, xsp,
+    _check((_lib or lib()).sp24_moe_sort(xp, dt, _arg(routing, "routing", dev, (T, topk), torch.int32), T, topk, E, H, xsp,
                                _arg(pos, "pos", dev, (T, topk), torch.int32), _arg(src, "src", dev, (n,), torch.int32),
                                _arg(row_expert, "row_expert", dev, (n,), torch.int32),
                                _arg(offsets, "offsets", dev, (E + 1,), torch.int32), wp, wn, _raw_stream(dev)),
@@ -992,7 +995,7 @@ def moe_sort_tables(routing: torch.Tensor, E: int, out=None, workspace=None) -> 
 
 
 def _unsort(ys, pos, router_w, dtype, out):
-    dev = ys.device
+    dev = ys.get_device()
     rows, H = _dims(ys, "ys", 2)
     T, topk = _dims(pos, "pos", 2)
     yp = _arg(ys, "ys", dev, ys.shape, *_FLOATS)
@@ -1001,7 +1004,7 @@ def _unsort(ys, pos, router_w, dtype, out):
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out must be {dtype}, not {out.dtype}")
     wp = None if router_w is None else _arg(router_w, "router_w", dev, (T, topk), torch.float32)
-    _check(lib().sp24_moe_unsort(yp, _DT[ys.dtype], _arg(pos, "pos", dev, (T, topk), torch.int32), wp, T, topk, rows, H,
+    _check((_lib or lib()).sp24_moe_unsort(yp, _DT[ys.dtype], _arg(pos, "pos", dev, (T, topk), torch.int32), wp, T, topk, rows, H,
                                  _arg(out, "out", dev, (T, H), *_FLOATS), _DT[out.dtype], _raw_stream(dev)),
            "sp24_moe_unsort")
     return out
@@ -1025,7 +1028,7 @@ def moe_unsort_backward(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, r
                         out=None):
     """(dys, d_router_w) of moe_unsort; rows of dys that no slot names are not written (zeros when
     allocated here).  Without router_w, d_router_w is None."""
-    dev = ys.device
+    dev = ys.get_device()
     rows, H = _dims(ys, "ys", 2)
     T, topk = _dims(pos, "pos", 2)
     yp = _arg(ys, "ys", dev, ys.shape, *_FLOATS)
@@ -1034,7 +1037,7 @@ def moe_unsort_backward(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, r
     dys, dw = out
     wp = None if router_w is None else _arg(router_w, "router_w", dev, (T, topk), torch.float32)
     dwp = None if dw is None else _arg(dw, "d_router_w", dev, (T, topk), torch.float32)
-    _check(lib().sp24_moe_unsort_backward(_arg(dy, "dy", dev, (T, H), *_FLOATS), _DT[dy.dtype], yp, _DT[ys.dtype],
+    _check((_lib or lib()).sp24_moe_unsort_backward(_arg(dy, "dy", dev, (T, H), *_FLOATS), _DT[dy.dtype], yp, _DT[ys.dtype],
                                           _arg(pos, "pos", dev, (T, topk), torch.int32), wp, T, topk, rows, H,
                                           _arg(dys, "dys", dev, (rows, H), ys.dtype), dwp, _raw_stream(dev)),
            "sp24_moe_unsort_backward")
@@ -1051,7 +1054,10 @@ class W4Tensor(NamedTuple):
     zeros: Optional[torch.Tensor] = None
 
 
-def _w4(w: W4Tensor, dev: torch.device):
+_pack_w4 = struct.Struct("iiPPP").pack  # _W4Operand's bytes, cheaper to make
+
+
+def _w4(w: W4Tensor, dev: int):
     """(C operand, rows, K) of 4-bit weights on `dev`."""
     rows, half = _dims(w.codes, "codes", 2)
     K = 2 * half
@@ -1059,9 +1065,9 @@ def _w4(w: W4Tensor, dev: torch.device):
     group = K // groups if groups else 128
     if groups * group != K:
         raise ValueError(f"{groups} groups do not divide {K} entries")
-    op = _W4Operand(_DT.get(w.scales.dtype, -1), group, _arg(w.codes, "codes", dev, (rows, half), torch.uint8),
-                    _arg(w.scales, "scales", dev, (rows, groups), *_HALVES),
-                    None if w.zeros is None else _arg(w.zeros, "zeros", dev, (rows, groups), torch.uint8))
+    op = _pack_w4(_DT.get(w.scales.dtype, -1), group, _arg(w.codes, "codes", dev, (rows, half), torch.uint8),
+                  _arg(w.scales, "scales", dev, (rows, groups), *_HALVES),
+                  0 if w.zeros is None else _arg(w.zeros, "zeros", dev, (rows, groups), torch.uint8))
     return op, rows, K
 
 
@@ -1069,7 +1075,7 @@ def _w4(w: W4Tensor, dev: torch.device):
 def quantize_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, out: Optional[W4Tensor] = None) -> W4Tensor:
     """4-bit codes of a 16-bit weight [rows, K], rounded to nearest, with one scale per `group`
     entries (symmetric), or with a zero point beside each scale."""
-    dev = w.device
+    dev = w.get_device()
     R, K = _dims(w, "w", 2)
     wp = _arg(w, "w", dev, w.shape, *_HALVES)
     if group not in (32, 64, 128) or K % group:
@@ -1079,7 +1085,7 @@ def quantize_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, out: Opt
                        torch.empty((R, K // group), dtype=w.dtype, device=dev),
                        torch.empty((R, K // group), dtype=torch.uint8, device=dev) if zeros else None)
     zp = _arg(out.zeros, "zeros", dev, (R, K // group), torch.uint8) if zeros else None
-    _check(lib().sp24_quantize_w4(wp, _DT[w.dtype], R, K, group, bool(zeros),
+    _check((_lib or lib()).sp24_quantize_w4(wp, _DT[w.dtype], R, K, group, bool(zeros),
                                   _arg(out.codes, "codes", dev, (R, K // 2), torch.uint8),
                                   _arg(out.scales, "scales", dev, (R, K // group), w.dtype), zp, _raw_stream(dev)),
            "sp24_quantize_w4")
@@ -1089,11 +1095,11 @@ def quantize_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, out: Opt
 @_placed
 def dequantize_w4(w: W4Tensor, dtype=torch.float32, out=None) -> torch.Tensor:
     """The values (q - z) * s of 4-bit weights, rounded once to `dtype`."""
-    dev = w.codes.device
+    dev = w.codes.get_device()
     op, rows, K = _w4(w, dev)
     if out is None:
         out = torch.empty((rows, K), dtype=dtype, device=dev)
-    _check(lib().sp24_dequantize_w4(ctypes.byref(op), rows, K, _DT[dtype], _arg(out, "out", dev, (rows, K), dtype),
+    _check((_lib or lib()).sp24_dequantize_w4(op, rows, K, _DT[dtype], _arg(out, "out", dev, (rows, K), dtype),
                                     _raw_stream(dev)), "sp24_dequantize_w4")
     return out
 
@@ -1104,21 +1110,21 @@ def _gemv_out(x, rows: int, N: int, act: int, dtype, out):
         out = torch.empty((rows, cols), dtype=dtype or (x.dtype if act == ACT_SWIGLU else torch.float32), device=x.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out must be {dtype}, not {out.dtype}")
-    return out, _arg(out, "out", x.device, (rows, cols), torch.float32, x.dtype)
+    return out, _arg(out, "out", x.get_device(), (rows, cols), torch.float32, x.dtype)
 
 
 @_placed
 def gemv_w4(x: torch.Tensor, w: W4Tensor, act: int = ACT_NONE, dtype=None, out=None) -> torch.Tensor:
     """y[M, N] = x[M, K] @ value(w)[N, K]^T for a few rows x (f16 / bf16), fp32 (or x's type by
     `dtype`); ACT_SWIGLU: w holds gate rows then up rows, y[M, N/2] = SiLU(gate) * up in x's type."""
-    dev = x.device
+    dev = x.get_device()
     M, K = _dims(x, "x", 2)
     xp = _arg(x, "x", dev, x.shape, *_HALVES)
     op, N, Kw = _w4(w, dev)
     if K != Kw:
         raise ValueError(f"K mismatch: {K} vs {Kw}")
     out, yp = _gemv_out(x, M, N, act, dtype, out)
-    _check(lib().sp24_gemv_w4(xp, _DT[x.dtype], ctypes.byref(op), M, N, K, act, yp, _DT[out.dtype], _raw_stream(dev)),
+    _check((_lib or lib()).sp24_gemv_w4(xp, _DT[x.dtype], op, M, N, K, act, yp, _DT[out.dtype], _raw_stream(dev)),
            "sp24_gemv_w4")
     return out
 
@@ -1128,7 +1134,7 @@ def gemv_w4_grouped(xs: torch.Tensor, w: W4Tensor, offsets: torch.Tensor, act: i
                     out=None) -> torch.Tensor:
     """gemv_w4 over rows in expert order (moe_sort's xs and offsets [E + 1]) with the E matrices
     stacked in w; rows from offsets[E] on are not written (zeros when allocated here)."""
-    dev = xs.device
+    dev = xs.get_device()
     R, K = _dims(xs, "xs", 2)
     xp = _arg(xs, "xs", dev, xs.shape, *_HALVES)
     op, rows, Kw = _w4(w, dev)
@@ -1142,6 +1148,6 @@ def gemv_w4_grouped(xs: torch.Tensor, w: W4Tensor, offsets: torch.Tensor, act: i
         cols = N // 2 if act == ACT_SWIGLU else N
         out = torch.zeros((R, cols), dtype=dtype or (xs.dtype if act == ACT_SWIGLU else torch.float32), device=dev)
     out, yp = _gemv_out(xs, R, N, act, dtype, out)
-    _check(lib().sp24_gemv_w4_grouped(xp, _DT[xs.dtype], ctypes.byref(op), _arg(offsets, "offsets", dev, (E + 1,), torch.int32),
+    _check((_lib or lib()).sp24_gemv_w4_grouped(xp, _DT[xs.dtype], op, _arg(offsets, "offsets", dev, (E + 1,), torch.int32),
                                       R, E, N, K, act, yp, _DT[out.dtype], _raw_stream(dev)), "sp24_gemv_w4_grouped")
     return out

@@ -15,154 +15,290 @@ constexpr int kCounters = 8192;  // counters of one pass over a chunk (32 KB of 
 
 // ------------------------------------------------------------------ element access
 
-template <int DT>
-struct Elem;
-template <>
-struct Elem<SP24_F32> {
-  using T = float;
-  static __device__ __forceinline__ float get(T v) { return v; }
-  static __device__ __forceinline__ T put(float v) { return v; }
-};
-template <>
-struct Elem<SP24_BF16> {
-  using T = __nv_bfloat16;
-  static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
-  static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
-};
-template <>
-struct Elem<SP24_F16> {
-  using T = __half;
-  static __device__ __forceinline__ float get(T v) { return __half2float(v); }
-  static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
+// V consecutive elements of type DT as 32-bit words (one half word for a single 16-bit element), moved
+// with accesses of at most 16 bytes, whatever the vector's size.
+template <int BYTES>
+struct Words {
+  uint32_t w[BYTES < 4 ? 1 : BYTES / 4];
 };
 
-// V consecutive elements moved with one access.
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T e[V];
+template <int BYTES>
+__device__ __forceinline__ Words<BYTES> load_words(const void* base, int64_t index) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + index * BYTES;
+  Words<BYTES> r;
+  if constexpr (BYTES == 2) {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  } else if constexpr (BYTES == 4) {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+  }
+  return r;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void store_words(void* base, int64_t index, const Words<BYTES>& r) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(base) + index * BYTES;
+  if constexpr (BYTES == 2) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)r.w[0];
+  } else if constexpr (BYTES == 4) {
+    *reinterpret_cast<uint32_t*>(p) = r.w[0];
+  } else if constexpr (BYTES == 8) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i)
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+  }
+}
+
+template <int DT>
+struct Elem {
+  static constexpr int kBytes = DT == SP24_F32 ? 4 : 2;
+  // element k of a vector's words
+  template <int BYTES>
+  static __device__ __forceinline__ float get(const Words<BYTES>& v, int k) {
+    if (DT == SP24_F32) return __uint_as_float(v.w[k]);
+    const uint32_t word = v.w[k / 2];
+    if (DT == SP24_BF16) return __uint_as_float(k & 1 ? word & 0xffff0000u : word << 16);
+    return __half2float(__ushort_as_half((unsigned short)(k & 1 ? word >> 16 : word & 0xffffu)));
+  }
+  static __device__ __forceinline__ uint32_t bits(float v) {
+    if (DT == SP24_F32) return __float_as_uint(v);
+    return DT == SP24_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+  }
+  template <int V>
+  static __device__ __forceinline__ Words<V * kBytes> put(const float (&f)[V]) {
+    Words<V * kBytes> r;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (DT == SP24_F32)
+        r.w[k] = bits(f[k]);
+      else if (k % 2 == 0)
+        r.w[k / 2] = bits(f[k]);
+      else
+        r.w[k / 2] |= bits(f[k]) << 16;
+    }
+    return r;
+  }
 };
 
 // ------------------------------------------------------------------ sort
 //
-// The row of entry i is the number of entries before it in the order (expert, entry number).  One
-// warp finds it by counting and then moves the entry's row of x.
+// The row of entry i is the number of entries before it in the order (expert, entry number).
 //
-// Few entries: every warp counts over all of them, in one launch.  Many: the entries are cut into
-// chunks of 2^chunk_log; a first launch counts each chunk's entries per expert (and all of them, by
-// integer atomics, whose order does not matter), and the warp adds up the totals of lower experts, its
-// expert's counts in earlier chunks and the equal entries before it in its own chunk.  Its reads grow
-// like E + n / chunk + chunk instead of n, so the chunk is about sqrt(n).
+// Few entries: one warp per entry counts over all of them and moves the entry's row of x, in one
+// launch.  Many: three.  The entries are cut into chunks of about sqrt(n); the first launch counts
+// each chunk's entries per expert, the second turns an expert's counts into those of earlier chunks
+// (one warp per expert) and its last CTA to finish adds up the experts' offsets, the third adds to
+// both the equal entries before entry i in its own chunk, and moves the rows.
 
 struct SortTables {
   const int32_t* routing;
   int64_t n, E;
   int32_t *pos, *src, *row_expert, *offsets;
-  const int32_t* counts;  // [E + 1][chunks]: by expert (E: the empty slots), then by chunk
-  const int32_t* totals;  // [E + 1]
+  const int32_t* before;  // [E + 1][chunks]: entries of expert e (E: the empty slots) in earlier chunks
+  const int32_t* first;   // [E + 1]: entries of lower experts
   int64_t chunks;
   int chunk_log;
 };
 
 // The expert of an entry; empty slots come after every expert.
-__device__ __forceinline__ int64_t entry_key(int32_t id, int64_t E) { return id < 0 || id >= E ? E : id; }
+__device__ __forceinline__ int entry_key(int32_t id, int64_t E) { return id < 0 || id >= E ? (int)E : id; }
 
-template <bool MANY>
-__device__ __forceinline__ int entries_below(const SortTables& t, int64_t key) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  if (MANY) {
-    for (int64_t e = lane; e < key; e += 32) before += t.totals[e];
-  } else {
-    for (int64_t j = lane; j < t.n; j += 32) before += entry_key(t.routing[j], t.E) < key;
-  }
-  return before;
+__device__ __forceinline__ void put_entry(const SortTables& t, int64_t i, int key, int row) {
+  const bool held = key < t.E;
+  t.pos[i] = held ? row : -1;
+  t.src[row] = held ? (int32_t)i : -1;
+  t.row_expert[row] = held ? key : -1;
 }
 
-template <bool MANY>
-__device__ __forceinline__ int equal_before(const SortTables& t, int64_t key, int64_t i) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  int64_t from = 0;
-  if (MANY) {
-    const int64_t chunk = i >> t.chunk_log;
-    const int32_t* const mine = t.counts + key * t.chunks;
-    for (int64_t c = lane; c < chunk; c += 32) before += mine[c];
-    from = chunk << t.chunk_log;
+// A warp copies a row of `vecs` vectors, kBatch loads in flight per lane.
+constexpr int kBatch = 8;
+template <int BYTES>
+__device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t vecs) {
+  int64_t c = threadIdx.x & 31;
+  for (; c + 32 * (kBatch - 1) < vecs; c += 32 * kBatch) {
+    Words<BYTES> v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) v[k] = load_words<BYTES>(from, c + 32 * k);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) store_words<BYTES>(to, c + 32 * k, v[k]);
   }
-  for (int64_t j = from + lane; j < i; j += 32) before += entry_key(t.routing[j], t.E) == key;
-  return before;
+  for (; c < vecs; c += 32) store_words<BYTES>(to, c, load_words<BYTES>(from, c));
 }
 
 // One warp per entry, then one per offset.
-template <int BYTES, bool MANY>
-__global__ void __launch_bounds__(32 * kWarps) sort_kernel(const __grid_constant__ SortTables t,
-                                                           const uint8_t* __restrict__ x, int topk, int64_t row_bytes,
-                                                           uint8_t* __restrict__ xs) {
+template <int BYTES>
+__global__ void __launch_bounds__(32 * kWarps) sort_few_kernel(const __grid_constant__ SortTables t,
+                                                               const uint8_t* __restrict__ x, int topk,
+                                                               int64_t row_bytes, uint8_t* __restrict__ xs) {
   const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= t.n + t.E + 1) return;
-  if (i >= t.n) {
-    const int at = __reduce_add_sync(kFull, entries_below<MANY>(t, i - t.n));
-    if (lane == 0) t.offsets[i - t.n] = at;
+  const int i = blockIdx.x * kWarps + (threadIdx.x >> 5), n = (int)t.n;
+  if (i >= n + t.E + 1) return;
+  const int32_t id = i < n ? t.routing[i] : i - n;
+  const int key = entry_key(id, t.E);
+  int before = 0;  // i >= n: all entries of lower experts
+  for (int j = lane; j < n; j += 32) {
+    const int k = entry_key(t.routing[j], t.E);
+    before += k < key || (k == key && j < i && i < n);
+  }
+  before = __reduce_add_sync(kFull, before);
+  if (i >= n) {
+    if (lane == 0) t.offsets[i - n] = before;
     return;
   }
-  const int32_t id = t.routing[i];
-  const int64_t key = entry_key(id, t.E);
-  const bool held = key < t.E;
-  if (!held && id != -1 && lane == 0) set_dev_error(SP24_ERR_INVALID_ARG);
-  const int row = __reduce_add_sync(kFull, entries_below<MANY>(t, key) + equal_before<MANY>(t, key, i));
   if (lane == 0) {
-    t.pos[i] = held ? row : -1;
-    t.src[row] = held ? (int32_t)i : -1;
-    t.row_expert[row] = held ? id : -1;
+    if (key == t.E && id != -1) set_dev_error(SP24_ERR_INVALID_ARG);
+    put_entry(t, i, key, before);
   }
-  if (!held || !x) return;
-  using V = Vec<uint8_t, BYTES>;
-  const V* from = reinterpret_cast<const V*>(x + (i / topk) * row_bytes);
-  V* to = reinterpret_cast<V*>(xs + (int64_t)row * row_bytes);
-  for (int64_t c = lane; c < row_bytes / BYTES; c += 32) to[c] = from[c];
+  if (key == t.E || !x) return;
+  copy_row<BYTES>(xs + (int64_t)before * row_bytes, x + (i / topk) * row_bytes, row_bytes / BYTES);
 }
 
-// Each CTA counts one chunk; with E + 1 counters in shared memory.
+// Each CTA counts one chunk, kCounters experts at a time.
 __global__ void __launch_bounds__(256) sort_count_kernel(const int32_t* __restrict__ routing, int64_t n, int64_t E,
                                                          int chunk_log, int64_t chunks, int32_t* __restrict__ counts,
-                                                         int32_t* __restrict__ totals) {
+                                                         int32_t* __restrict__ done) {
   extern __shared__ int32_t held[];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
   const int64_t from = (int64_t)blockIdx.x << chunk_log, to = min(n, from + ((int64_t)1 << chunk_log));
-  for (int64_t e0 = 0; e0 <= E; e0 += kCounters) {
+  for (int e0 = 0; e0 <= E; e0 += kCounters) {
     const int span = (int)min((int64_t)kCounters, E + 1 - e0);
     for (int e = threadIdx.x; e < span; e += 256) held[e] = 0;
     __syncthreads();
     for (int64_t j = from + threadIdx.x; j < to; j += 256) {
-      const int64_t key = entry_key(routing[j], E) - e0;
+      const int key = entry_key(routing[j], E) - e0;
       if (key >= 0 && key < span) atomicAdd(&held[key], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < span; e += 256) {
-      const int32_t v = held[e];
-      counts[(e0 + e) * chunks + blockIdx.x] = v;
-      if (v) atomicAdd(&totals[e0 + e], v);
-    }
+    for (int e = threadIdx.x; e < span; e += 256) counts[(int64_t)(e0 + e) * chunks + blockIdx.x] = held[e];
     __syncthreads();
   }
 }
 
-// Above this many entries the chunked form is used: see sp24_moe_sort.
-constexpr int64_t kFew = 2048;
+__device__ __forceinline__ int warp_scan(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kFull, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// One warp per expert: its counts become those of earlier chunks.  The CTA that finishes last (a
+// counter tells; nobody waits) turns the totals into `first` and the offsets.
+__global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restrict__ counts, int64_t E, int64_t chunks,
+                                                                int32_t* __restrict__ first,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ done) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t e = (int64_t)blockIdx.x * kWarps + warp;
+  if (e <= E) {
+    int32_t* const mine = counts + e * chunks;
+    int carry = 0;
+    for (int64_t c0 = 0; c0 < chunks; c0 += 32 * kBatch) {
+      int v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) v[k] = c0 + 32 * k + lane < chunks ? mine[c0 + 32 * k + lane] : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int upto = warp_scan(v[k]);
+        if (c0 + 32 * k + lane < chunks) mine[c0 + 32 * k + lane] = carry + upto - v[k];
+        carry += __shfl_sync(kFull, upto, 31);
+      }
+    }
+    if (lane == 0) first[e] = carry;
+  }
+  __shared__ int last;
+  __shared__ int sums[kWarps];
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(done, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  int carry = 0;
+  for (int64_t e0 = 0; e0 <= E; e0 += 32 * kWarps) {
+    const int64_t at = e0 + threadIdx.x;
+    const int v = at <= E ? __ldcg(first + at) : 0;
+    const int upto = warp_scan(v);
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int base = carry;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += sums[w];
+      carry += sums[w];
+    }
+    if (at <= E) first[at] = offsets[at] = base + upto - v;
+    __syncthreads();
+  }
+}
+
+// kEntries entries per CTA, kParts threads each for the place within the chunk, then one warp per row.
+constexpr int kEntries = 32;
+constexpr int kParts = 8;
+constexpr int kMaxChunkLog = 11;
+template <int BYTES>
+__global__ void __launch_bounds__(kParts * kEntries) sort_many_kernel(const __grid_constant__ SortTables t,
+                                                                 const uint8_t* __restrict__ x, int topk,
+                                                                 int64_t row_bytes, uint8_t* __restrict__ xs) {
+  __shared__ int32_t keys[1 << kMaxChunkLog];  // from the chunk's first entry to this CTA's last
+  __shared__ int rows[kEntries];
+  const int64_t i0 = (int64_t)blockIdx.x * kEntries, from = i0 >> t.chunk_log << t.chunk_log;
+  const int mine = (int)min((int64_t)kEntries, t.n - i0), ahead = (int)(i0 - from);
+  for (int j = threadIdx.x; j < ahead + mine; j += kParts * kEntries) {
+    const int32_t id = t.routing[from + j];
+    const int key = entry_key(id, t.E);
+    if (key == t.E && id != -1 && j >= ahead) set_dev_error(SP24_ERR_INVALID_ARG);
+    keys[j] = key;
+  }
+  __syncthreads();
+  const int i = threadIdx.x / kParts, part = threadIdx.x % kParts;
+  const int key = i < mine ? keys[ahead + i] : 0;
+  int base = 0, equal = 0;
+  if (i < mine && part == 0) base = t.first[key] + t.before[key * t.chunks + (i0 >> t.chunk_log)];
+  if (i < mine)
+    for (int j = part; j < ahead + i; j += kParts) equal += keys[j] == key;
+#pragma unroll
+  for (int d = 1; d < kParts; d <<= 1) equal += __shfl_xor_sync(kFull, equal, d);
+  if (i < mine && part == 0) {
+    const int row = base + equal;
+    put_entry(t, i0 + i, key, row);
+    rows[i] = key < t.E ? row : -1;
+  }
+  if (!x) return;
+  __syncthreads();
+  for (int e = threadIdx.x >> 5; e < mine; e += kParts * kEntries / 32)
+    if (rows[e] >= 0)
+      copy_row<BYTES>(xs + (int64_t)rows[e] * row_bytes, x + (i0 + e) / topk * row_bytes, row_bytes / BYTES);
+}
+
+// Above this many entries the counts are made by chunk: see sp24_moe_sort.
+constexpr int64_t kFew = 1024;
 
 struct SortWs {
   int chunk_log;
-  int64_t chunks, totals_at, counts_at, bytes;
+  int64_t chunks, first_at, before_at, bytes;
 };
 
 SortWs sort_layout(int64_t n, int64_t E) {
   SortWs w{};
   if (n <= kFew) return w;
   w.chunk_log = 8;
-  while ((1ll << (2 * w.chunk_log)) < n) ++w.chunk_log;
-  w.chunks = (n + (1ll << w.chunk_log) - 1) >> w.chunk_log;
-  w.counts_at = ((E + 1) * 4 + 15) / 16 * 16;
-  w.bytes = w.counts_at + (E + 1) * w.chunks * 4;
+  while (w.chunk_log < kMaxChunkLog && ((int64_t)1 << (2 * w.chunk_log)) < n) ++w.chunk_log;
+  w.chunks = (n + ((int64_t)1 << w.chunk_log) - 1) >> w.chunk_log;
+  w.first_at = 16;
+  w.before_at = w.first_at + ((E + 1) * 4 + 15) / 16 * 16;
+  w.bytes = w.before_at + (E + 1) * w.chunks * 4;
   return w;
 }
 
@@ -176,71 +312,109 @@ __device__ __forceinline__ int entry_row(const int32_t* pos, int64_t i, int64_t 
   return -1;
 }
 
-// One thread per V columns of one token; the slots in order.
-template <int YS, int Y, int V>
-__global__ void __launch_bounds__(256) unsort_kernel(const void* __restrict__ ys_, const int32_t* __restrict__ pos,
-                                                     const float* __restrict__ router_w, int64_t T, int topk,
-                                                     int64_t rows, int64_t H, void* __restrict__ y_) {
-  using VI = Vec<typename Elem<YS>::T, V>;
-  using VO = Vec<typename Elem<Y>::T, V>;
-  const VI* ys = reinterpret_cast<const VI*>(ys_);
-  VO* y = reinterpret_cast<VO*>(y_);
-  const int64_t HV = H / V, total = T * HV;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / HV, c = i - t * HV;
-    float acc[V];
+// One warp per 32 W vectors of V columns of one token; the slots in order, kSlots of them in flight.
+constexpr int kSlots = 5;
+template <int YS, int Y, int V, int W>
+__global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restrict__ ys,
+                                                             const int32_t* __restrict__ pos,
+                                                             const float* __restrict__ router_w, uint32_t units,
+                                                             uint32_t per_row, int topk, int64_t rows, int64_t HV,
+                                                             void* __restrict__ y) {
+  constexpr int kIn = V * Elem<YS>::kBytes, kOut = V * Elem<Y>::kBytes;
+  const int lane = threadIdx.x & 31;
+  const uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= units) return;
+  const uint32_t t = u / per_row;
+  const int64_t c = (int64_t)(u - t * per_row) * (32 * W) + lane;
+  const int32_t* const my_pos = pos + (int64_t)t * topk;
+  const float* const my_w = router_w + (int64_t)t * topk;
+  float acc[W][V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-    for (int s = 0; s < topk; ++s) {
-      const int r = entry_row(pos, t * topk + s, rows);
-      if (r < 0) continue;
-      const float w = router_w ? router_w[t * topk + s] : 1.0f;
-      const VI v = ys[r * HV + c];
+  for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] = fmaf(w, Elem<YS>::get(v.e[k]), acc[k]);
+    for (int k = 0; k < V; ++k) acc[j][k] = 0.0f;
+  for (int s0 = 0; s0 < topk; s0 += kSlots) {
+    int r[kSlots];
+    float w[kSlots];
+    Words<kIn> v[kSlots][W];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      const bool slot = s0 + s < topk;
+      r[s] = slot ? my_pos[s0 + s] : -1;
+      w[s] = slot && router_w ? my_w[s0 + s] : 1.0f;
     }
-    VO o;
 #pragma unroll
-    for (int k = 0; k < V; ++k) o.e[k] = Elem<Y>::put(acc[k]);
-    y[i] = o;
+    for (int s = 0; s < kSlots; ++s) {
+      const bool held = r[s] >= 0 && r[s] < rows;
+      if (!held && r[s] != -1) set_dev_error(SP24_ERR_INVALID_ARG);
+      w[s] = held ? w[s] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        v[s][j] = Words<kIn>{};
+        if (held && c + 32 * j < HV) v[s][j] = load_words<kIn>(ys, r[s] * HV + c + 32 * j);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[j][k] = fmaf(w[s], Elem<YS>::get(v[s][j], k), acc[j][k]);
   }
+#pragma unroll
+  for (int j = 0; j < W; ++j)
+    if (c + 32 * j < HV) store_words<kOut>(y, (int64_t)t * HV + c + 32 * j, Elem<Y>::put(acc[j]));
 }
 
-// One warp per entry: its row of dys, and the dot product that is its weight's gradient.
-template <int YS, int Y, int V>
+// One warp per entry: its row of dys, and (DOT) the dot product that is its weight's gradient; kPairs
+// loads of either row in flight per lane.
+constexpr int kPairs = 4;
+template <int YS, int Y, int V, bool DOT>
 __global__ void __launch_bounds__(32 * kWarps) unsort_backward_kernel(
-    const void* __restrict__ dy_, const void* __restrict__ ys_, const int32_t* __restrict__ pos,
-    const float* __restrict__ router_w, int64_t n, int topk, int64_t rows, int64_t H, void* __restrict__ dys_,
+    const void* __restrict__ dy, const void* __restrict__ ys, const int32_t* __restrict__ pos,
+    const float* __restrict__ router_w, int64_t n, int topk, int64_t rows, int64_t HV, void* __restrict__ dys,
     float* __restrict__ d_router_w) {
-  using VI = Vec<typename Elem<YS>::T, V>;
-  using VO = Vec<typename Elem<Y>::T, V>;
+  constexpr int kIn = V * Elem<YS>::kBytes, kOut = V * Elem<Y>::kBytes;
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= n) return;
   const int r = entry_row(pos, i, rows);
   if (r < 0) {
-    if (d_router_w && lane == 0) d_router_w[i] = 0.0f;
+    if (DOT && lane == 0) d_router_w[i] = 0.0f;
     return;
   }
   const float w = router_w ? router_w[i] : 1.0f;
-  const int64_t HV = H / V;
-  const VO* dy = reinterpret_cast<const VO*>(dy_) + (i / topk) * HV;
-  const VI* ys = reinterpret_cast<const VI*>(ys_) + r * HV;
-  VI* dys = reinterpret_cast<VI*>(dys_) + r * HV;
+  const int64_t from = (int64_t)((uint32_t)i / (uint32_t)topk) * HV, at = r * HV;
   float dot = 0.0f;
-  for (int64_t c = lane; c < HV; c += 32) {
-    const VO g = dy[c];
-    VI d;
-    if (d_router_w) {
-      const VI v = ys[c];
+  auto step = [&](int64_t c, const Words<kOut>& g, const Words<kIn>& v) {
+    float d[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) dot = fmaf(Elem<Y>::get(g.e[k]), Elem<YS>::get(v.e[k]), dot);
+    for (int k = 0; k < V; ++k) {
+      const float a = Elem<Y>::get(g, k);
+      if (DOT) dot = fmaf(a, Elem<YS>::get(v, k), dot);
+      d[k] = w * a;
+    }
+    store_words<kIn>(dys, at + c, Elem<YS>::put(d));
+  };
+  int64_t c = lane;
+  for (; c + 32 * (kPairs - 1) < HV; c += 32 * kPairs) {
+    Words<kOut> g[kPairs];
+    Words<kIn> v[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      g[j] = load_words<kOut>(dy, from + c + 32 * j);
+      v[j] = Words<kIn>{};
+      if (DOT) v[j] = load_words<kIn>(ys, at + c + 32 * j);
     }
 #pragma unroll
-    for (int k = 0; k < V; ++k) d.e[k] = Elem<YS>::put(w * Elem<Y>::get(g.e[k]));
-    dys[c] = d;
+    for (int j = 0; j < kPairs; ++j) step(c + 32 * j, g[j], v[j]);
   }
-  if (d_router_w) {
+  for (; c < HV; c += 32) {
+    Words<kIn> v{};
+    if (DOT) v = load_words<kIn>(ys, at + c);
+    step(c, load_words<kOut>(dy, from + c), v);
+  }
+  if (DOT) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
     if (lane == 0) d_router_w[i] = dot;
@@ -292,7 +466,7 @@ using namespace sp24;
 extern "C" int sp24_moe_sort_workspace_size(int64_t T, int topk, int64_t E, int64_t* bytes) {
   if (!bytes) return SP24_ERR_INVALID_ARG;
   if (T < 0 || topk < 1 || E < 1) return SP24_ERR_SHAPE;
-  if (E > (1 << 20) || T > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
+  if (E > (1 << 16) || T > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
   *bytes = sort_layout(T * topk, E).bytes;
   return SP24_OK;
 }
@@ -303,7 +477,7 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   const int eb = elem_bytes(dtype);
   if (!eb) return SP24_ERR_DTYPE;
   if (T < 0 || topk < 1 || E < 1 || H < 0) return SP24_ERR_SHAPE;
-  if (E > (1 << 20) || T > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
+  if (E > (1 << 16) || T > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
   const int64_t n = T * topk;
   if (!offsets || (n && (!routing || !pos || !src || !row_expert))) return SP24_ERR_INVALID_ARG;
   if (n && H && !x != !xs) return SP24_ERR_INVALID_ARG;
@@ -315,28 +489,32 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   if (ws.bytes && !aligned(workspace, 16)) return SP24_ERR_ALIGN;
   cudaStream_t s = as_stream(stream);
   SortTables t{routing, n, E, pos, src, row_expert, offsets, nullptr, nullptr, ws.chunks, ws.chunk_log};
+  int st = SP24_OK;
   if (ws.bytes) {
-    int32_t* totals = reinterpret_cast<int32_t*>(workspace);
-    int32_t* counts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) + ws.counts_at);
-    if (cudaMemsetAsync(totals, 0, (size_t)(E + 1) * 4, s) != cudaSuccess) return SP24_ERR_CUDA;
+    uint8_t* const base = reinterpret_cast<uint8_t*>(workspace);
+    int32_t* const done = reinterpret_cast<int32_t*>(base);
+    int32_t* const first = reinterpret_cast<int32_t*>(base + ws.first_at);
+    int32_t* const before = reinterpret_cast<int32_t*>(base + ws.before_at);
     const int64_t counters = E + 1 < kCounters ? E + 1 : kCounters;
     sort_count_kernel<<<(unsigned)ws.chunks, 256, (size_t)counters * 4, s>>>(routing, n, E, ws.chunk_log, ws.chunks,
-                                                                             counts, totals);
-    const int st = launch_status();
+                                                                             before, done);
+    st = launch_status();
     if (st) return st;
-    t.totals = totals;
-    t.counts = counts;
+    sort_scan_kernel<<<(unsigned)((E + kWarps) / kWarps), 32 * kWarps, 0, s>>>(before, E, ws.chunks, first, offsets, done);
+    st = launch_status();
+    if (st) return st;
+    t.first = first;
+    t.before = before;
   }
   const int64_t row = H * eb;
-  const unsigned ctas = (unsigned)((n + E + 1 + kWarps - 1) / kWarps);
   const uint8_t* from = H ? reinterpret_cast<const uint8_t*>(x) : nullptr;
   uint8_t* to = reinterpret_cast<uint8_t*>(xs);
   auto run = [&](auto bytes) {
     constexpr int B = decltype(bytes)::value;
     if (ws.bytes)
-      sort_kernel<B, true><<<ctas, 32 * kWarps, 0, s>>>(t, from, topk, row, to);
+      sort_many_kernel<B><<<(unsigned)((n + kEntries - 1) / kEntries), kParts * kEntries, 0, s>>>(t, from, topk, row, to);
     else
-      sort_kernel<B, false><<<ctas, 32 * kWarps, 0, s>>>(t, from, topk, row, to);
+      sort_few_kernel<B><<<(unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s>>>(t, from, topk, row, to);
     return launch_status();
   };
   if (row % 16 == 0 && aligned(x, 16) && aligned(xs, 16)) return run(std::integral_constant<int, 16>{});
@@ -357,9 +535,12 @@ extern "C" int sp24_moe_unsort(const void* ys, int ys_dtype, const int32_t* pos,
   return by_pair(ys_dtype, y_dtype, [&](auto p) {
     auto run = [&](auto vec) {
       constexpr int V = decltype(vec)::value;
-      const int64_t blocks = (T * (H / V) + 255) / 256, cap = (int64_t)sm_count() * 64;
-      unsort_kernel<decltype(p)::ys, decltype(p)::y, V><<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, s>>>(
-          ys, pos, router_w, T, topk, rows, H, y);
+      constexpr int W = V >= 4 ? 1 : 4 / V;
+      const int64_t per_row = (H / V + 32 * W - 1) / (32 * W), units = T * per_row;
+      if (units > INT32_MAX) return (int)SP24_ERR_UNSUPPORTED;  // more than any device's memory holds
+      unsort_kernel<decltype(p)::ys, decltype(p)::y, V, W>
+          <<<(unsigned)((units + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(
+              ys, pos, router_w, (uint32_t)units, (uint32_t)per_row, topk, rows, H / V, y);
       return launch_status();
     };
     if (v == 8) return run(std::integral_constant<int, 8>{});
@@ -385,9 +566,13 @@ extern "C" int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void*
   return by_pair(ys_dtype, y_dtype, [&](auto p) {
     auto run = [&](auto vec) {
       constexpr int V = decltype(vec)::value;
-      unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V>
-          <<<(unsigned)((n + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(dy, ys, pos, router_w, n, topk, rows, H, dys,
-                                                                         d_router_w);
+      const unsigned ctas = (unsigned)((n + kWarps - 1) / kWarps);
+      if (d_router_w)
+        unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, true>
+            <<<ctas, 32 * kWarps, 0, s>>>(dy, ys, pos, router_w, n, topk, rows, H / V, dys, d_router_w);
+      else
+        unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, false>
+            <<<ctas, 32 * kWarps, 0, s>>>(dy, ys, pos, router_w, n, topk, rows, H / V, dys, nullptr);
       return launch_status();
     };
     if (v == 8) return run(std::integral_constant<int, 8>{});

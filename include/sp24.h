@@ -547,7 +547,7 @@ int sp24_moe_route_backward(const void* logits, int dtype, const int32_t* routin
  * x (device, F32/F16/BF16, [T, H]) and xs may both be NULL: the tables only.  Ids outside [0, E)
  * other than -1 are empty slots too and set the device error word (SP24_ERR_INVALID_ARG).
  * The gradient of x is sp24_moe_unsort of xs's gradient with router_w NULL.
- * n up to 2^31 - 1, E up to 2^20 (SP24_ERR_UNSUPPORTED above).  n == 0 writes offsets only.
+ * n up to 2^31 - 1, E up to 2^16 (SP24_ERR_UNSUPPORTED above).  n == 0 writes offsets only.
  * workspace: sp24_moe_sort_workspace_size() bytes (may be 0), 16-byte aligned; scratch. */
 int sp24_moe_sort_workspace_size(int64_t T, int topk, int64_t E, int64_t* bytes);
 int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, int64_t T, int topk, int64_t E, int64_t H,

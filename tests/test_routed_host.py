@@ -32,7 +32,7 @@ def test_sort_refusals():
         return _raw("sp24_moe_sort", x, dt, r, T, k, E, H, xs, pos, src, re, off, None, 0, None)
     assert f(dt=sp.NVFP4) == sp.ERR_DTYPE
     assert f(T=-1) == f(k=0) == f(E=0) == f(H=-1) == sp.ERR_SHAPE
-    assert f(E=2**20 + 1) == f(T=2**30, k=2) == f(T=2**31) == sp.ERR_UNSUPPORTED
+    assert f(E=2**16 + 1) == f(T=2**30, k=2) == f(T=2**31) == sp.ERR_UNSUPPORTED
     assert f(pos=None) == f(src=None) == f(re=None) == f(off=None) == f(r=None) == sp.ERR_INVALID_ARG
     assert f(x=None) == f(xs=None) == sp.ERR_INVALID_ARG
     assert f(x=17) == f(xs=17) == f(pos=18) == f(off=18) == sp.ERR_ALIGN

@@ -132,7 +132,33 @@ __device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) store_words<BYTES>(to, c + 32 * k, v[k]);
   }
-  for (; c < vecs; c += 32) store_words<BYTES>(to, c, load_words<BYTES>(from, c));
+  for (; c + 32 < vecs; c += 64) {
+    const Words<BYTES> a = load_words<BYTES>(from, c), b = load_words<BYTES>(from, c + 32);
+    store_words<BYTES>(to, c, a);
+    store_words<BYTES>(to, c + 32, b);
+  }
+  if (c < vecs) store_words<BYTES>(to, c, load_words<BYTES>(from, c));
+}
+
+// Programmatic dependent launch: a kernel lets the next one of its stream start early, and that one
+// waits (in hardware) for its predecessor's end before it touches what that writes.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), unsigned ctas, unsigned threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  count_launch(1);
+  return e == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
 }
 
 // One warp per entry, then one per offset.
@@ -168,6 +194,7 @@ __global__ void __launch_bounds__(256) sort_count_kernel(const int32_t* __restri
                                                          int chunk_log, int64_t chunks, int32_t* __restrict__ counts,
                                                          int32_t* __restrict__ done) {
   extern __shared__ int32_t held[];
+  let_next_start();
   if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
   const int64_t from = (int64_t)blockIdx.x << chunk_log, to = min(n, from + ((int64_t)1 << chunk_log));
   for (int e0 = 0; e0 <= E; e0 += kCounters) {
@@ -202,6 +229,8 @@ __global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restr
                                                                 int32_t* __restrict__ done) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t e = (int64_t)blockIdx.x * kWarps + warp;
+  let_next_start();
+  wait_for_previous();
   if (e <= E) {
     int32_t* const mine = counts + e * chunks;
     int carry = 0;
@@ -264,14 +293,14 @@ __global__ void __launch_bounds__(kParts * kEntries) sort_many_kernel(const __gr
   __syncthreads();
   const int i = threadIdx.x / kParts, part = threadIdx.x % kParts;
   const int key = i < mine ? keys[ahead + i] : 0;
-  int base = 0, equal = 0;
-  if (i < mine && part == 0) base = t.first[key] + t.before[key * t.chunks + (i0 >> t.chunk_log)];
+  int equal = 0;
   if (i < mine)
     for (int j = part; j < ahead + i; j += kParts) equal += keys[j] == key;
 #pragma unroll
   for (int d = 1; d < kParts; d <<= 1) equal += __shfl_xor_sync(kFull, equal, d);
+  wait_for_previous();
   if (i < mine && part == 0) {
-    const int row = base + equal;
+    const int row = t.first[key] + t.before[key * t.chunks + (i0 >> t.chunk_log)] + equal;
     put_entry(t, i0 + i, key, row);
     rows[i] = key < t.E ? row : -1;
   }
@@ -283,7 +312,7 @@ __global__ void __launch_bounds__(kParts * kEntries) sort_many_kernel(const __gr
 }
 
 // Above this many entries the counts are made by chunk: see sp24_moe_sort.
-constexpr int64_t kFew = 1024;
+constexpr int64_t kFew = 2048;
 
 struct SortWs {
   int chunk_log;
@@ -313,8 +342,7 @@ __device__ __forceinline__ int entry_row(const int32_t* pos, int64_t i, int64_t 
 }
 
 // One warp per 32 W vectors of V columns of one token; the slots in order, kSlots of them in flight.
-constexpr int kSlots = 5;
-template <int YS, int Y, int V, int W>
+template <int YS, int Y, int V, int W, int kSlots>
 __global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restrict__ ys,
                                                              const int32_t* __restrict__ pos,
                                                              const float* __restrict__ router_w, uint32_t units,
@@ -500,8 +528,8 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
                                                                              before, done);
     st = launch_status();
     if (st) return st;
-    sort_scan_kernel<<<(unsigned)((E + kWarps) / kWarps), 32 * kWarps, 0, s>>>(before, E, ws.chunks, first, offsets, done);
-    st = launch_status();
+    st = launch_after(sort_scan_kernel, (unsigned)((E + kWarps) / kWarps), 32 * kWarps, s, before, E, ws.chunks, first,
+                      offsets, done);
     if (st) return st;
     t.first = first;
     t.before = before;
@@ -512,9 +540,9 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   auto run = [&](auto bytes) {
     constexpr int B = decltype(bytes)::value;
     if (ws.bytes)
-      sort_many_kernel<B><<<(unsigned)((n + kEntries - 1) / kEntries), kParts * kEntries, 0, s>>>(t, from, topk, row, to);
-    else
-      sort_few_kernel<B><<<(unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s>>>(t, from, topk, row, to);
+      return launch_after(sort_many_kernel<B>, (unsigned)((n + kEntries - 1) / kEntries), kParts * kEntries, s, t, from,
+                          topk, row, to);
+    sort_few_kernel<B><<<(unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s>>>(t, from, topk, row, to);
     return launch_status();
   };
   if (row % 16 == 0 && aligned(x, 16) && aligned(xs, 16)) return run(std::integral_constant<int, 16>{});
@@ -535,13 +563,19 @@ extern "C" int sp24_moe_unsort(const void* ys, int ys_dtype, const int32_t* pos,
   return by_pair(ys_dtype, y_dtype, [&](auto p) {
     auto run = [&](auto vec) {
       constexpr int V = decltype(vec)::value;
-      constexpr int W = V >= 4 ? 1 : 4 / V;
-      const int64_t per_row = (H / V + 32 * W - 1) / (32 * W), units = T * per_row;
-      if (units > INT32_MAX) return (int)SP24_ERR_UNSUPPORTED;  // more than any device's memory holds
-      unsort_kernel<decltype(p)::ys, decltype(p)::y, V, W>
-          <<<(unsigned)((units + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(
-              ys, pos, router_w, (uint32_t)units, (uint32_t)per_row, topk, rows, H / V, y);
-      return launch_status();
+      auto go = [&](auto wide, auto slots) {
+        constexpr int W = decltype(wide)::value, S = decltype(slots)::value;
+        const int64_t per_row = (H / V + 32 * W - 1) / (32 * W), units = T * per_row;
+        if (units > INT32_MAX) return (int)SP24_ERR_UNSUPPORTED;  // more than any device's memory holds
+        unsort_kernel<decltype(p)::ys, decltype(p)::y, V, W, S>
+            <<<(unsigned)((units + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(
+                ys, pos, router_w, (uint32_t)units, (uint32_t)per_row, topk, rows, H / V, y);
+        return launch_status();
+      };
+      constexpr int W = V >= 4 ? 2 : 8 / V;
+      if (topk <= 2) return go(std::integral_constant<int, W>{}, std::integral_constant<int, 2>{});
+      if (V <= 2) return go(std::integral_constant<int, W>{}, std::integral_constant<int, 2>{});
+      return go(std::integral_constant<int, 1>{}, std::integral_constant<int, 5>{});
     };
     if (v == 8) return run(std::integral_constant<int, 8>{});
     if (v == 4) return run(std::integral_constant<int, 4>{});

@@ -22,6 +22,29 @@ struct Words {
   uint32_t w[BYTES < 4 ? 1 : BYTES / 4];
 };
 
+// Rows of tens of thousands of entries pass through L2 once: they are read and written with the
+// evict-first policy, which leaves the tokens' own rows (read topk times) there.
+template <int BYTES>
+__device__ __forceinline__ Words<BYTES> load_stream(const void* base, int64_t index) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + index * BYTES;
+  Words<BYTES> r;
+  if constexpr (BYTES == 2) {
+    r.w[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
+  } else if constexpr (BYTES == 4) {
+    r.w[0] = __ldcs(reinterpret_cast<const unsigned int*>(p));
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+  }
+  return r;
+}
+
 template <int BYTES>
 __device__ __forceinline__ Words<BYTES> load_words(const void* base, int64_t index) {
   const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + index * BYTES;
@@ -44,18 +67,18 @@ __device__ __forceinline__ Words<BYTES> load_words(const void* base, int64_t ind
 }
 
 template <int BYTES>
-__device__ __forceinline__ void store_words(void* base, int64_t index, const Words<BYTES>& r) {
+__device__ __forceinline__ void store_stream(void* base, int64_t index, const Words<BYTES>& r) {
   uint8_t* p = reinterpret_cast<uint8_t*>(base) + index * BYTES;
   if constexpr (BYTES == 2) {
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)r.w[0];
+    __stcs(reinterpret_cast<unsigned short*>(p), (unsigned short)r.w[0]);
   } else if constexpr (BYTES == 4) {
-    *reinterpret_cast<uint32_t*>(p) = r.w[0];
+    __stcs(reinterpret_cast<unsigned int*>(p), r.w[0]);
   } else if constexpr (BYTES == 8) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(r.w[0], r.w[1]));
   } else {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+      __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]));
   }
 }
 
@@ -120,24 +143,24 @@ __device__ __forceinline__ void put_entry(const SortTables& t, int64_t i, int ke
   t.row_expert[row] = held ? key : -1;
 }
 
-// A warp copies a row of `vecs` vectors, kBatch loads in flight per lane.
-constexpr int kBatch = 8;
+// A warp copies a row of `vecs` vectors, 8 (then 4) loads in flight per lane.
+template <int BYTES, int BATCH>
+__device__ __forceinline__ void copy_batches(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t vecs,
+                                             int64_t& c) {
+  for (; c + 32 * (BATCH - 1) < vecs; c += 32 * BATCH) {
+    Words<BYTES> v[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) v[k] = load_words<BYTES>(from, c + 32 * k);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) store_stream<BYTES>(to, c + 32 * k, v[k]);
+  }
+}
 template <int BYTES>
 __device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t vecs) {
   int64_t c = threadIdx.x & 31;
-  for (; c + 32 * (kBatch - 1) < vecs; c += 32 * kBatch) {
-    Words<BYTES> v[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) v[k] = load_words<BYTES>(from, c + 32 * k);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) store_words<BYTES>(to, c + 32 * k, v[k]);
-  }
-  for (; c + 32 < vecs; c += 64) {
-    const Words<BYTES> a = load_words<BYTES>(from, c), b = load_words<BYTES>(from, c + 32);
-    store_words<BYTES>(to, c, a);
-    store_words<BYTES>(to, c + 32, b);
-  }
-  if (c < vecs) store_words<BYTES>(to, c, load_words<BYTES>(from, c));
+  copy_batches<BYTES, 8>(to, from, vecs, c);
+  copy_batches<BYTES, 4>(to, from, vecs, c);
+  copy_batches<BYTES, 1>(to, from, vecs, c);
 }
 
 // Programmatic dependent launch: a kernel lets the next one of its stream start early, and that one
@@ -211,6 +234,8 @@ __global__ void __launch_bounds__(256) sort_count_kernel(const int32_t* __restri
   }
 }
 
+constexpr int kScan = 8;  // counts in flight per lane
+
 __device__ __forceinline__ int warp_scan(int v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -234,12 +259,12 @@ __global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restr
   if (e <= E) {
     int32_t* const mine = counts + e * chunks;
     int carry = 0;
-    for (int64_t c0 = 0; c0 < chunks; c0 += 32 * kBatch) {
-      int v[kBatch];
+    for (int64_t c0 = 0; c0 < chunks; c0 += 32 * kScan) {
+      int v[kScan];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) v[k] = c0 + 32 * k + lane < chunks ? mine[c0 + 32 * k + lane] : 0;
+      for (int k = 0; k < kScan; ++k) v[k] = c0 + 32 * k + lane < chunks ? mine[c0 + 32 * k + lane] : 0;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < kScan; ++k) {
         const int upto = warp_scan(v[k]);
         if (c0 + 32 * k + lane < chunks) mine[c0 + 32 * k + lane] = carry + upto - v[k];
         carry += __shfl_sync(kFull, upto, 31);
@@ -379,7 +404,7 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restr
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         v[s][j] = Words<kIn>{};
-        if (held && c + 32 * j < HV) v[s][j] = load_words<kIn>(ys, r[s] * HV + c + 32 * j);
+        if (held && c + 32 * j < HV) v[s][j] = load_stream<kIn>(ys, r[s] * HV + c + 32 * j);
       }
     }
 #pragma unroll
@@ -391,7 +416,7 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restr
   }
 #pragma unroll
   for (int j = 0; j < W; ++j)
-    if (c + 32 * j < HV) store_words<kOut>(y, (int64_t)t * HV + c + 32 * j, Elem<Y>::put(acc[j]));
+    if (c + 32 * j < HV) store_stream<kOut>(y, (int64_t)t * HV + c + 32 * j, Elem<Y>::put(acc[j]));
 }
 
 // One warp per entry: its row of dys, and (DOT) the dot product that is its weight's gradient; kPairs
@@ -422,7 +447,7 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_backward_kernel(
       if (DOT) dot = fmaf(a, Elem<YS>::get(v, k), dot);
       d[k] = w * a;
     }
-    store_words<kIn>(dys, at + c, Elem<YS>::put(d));
+    store_stream<kIn>(dys, at + c, Elem<YS>::put(d));
   };
   int64_t c = lane;
   for (; c + 32 * (kPairs - 1) < HV; c += 32 * kPairs) {
@@ -432,14 +457,14 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_backward_kernel(
     for (int j = 0; j < kPairs; ++j) {
       g[j] = load_words<kOut>(dy, from + c + 32 * j);
       v[j] = Words<kIn>{};
-      if (DOT) v[j] = load_words<kIn>(ys, at + c + 32 * j);
+      if (DOT) v[j] = load_stream<kIn>(ys, at + c + 32 * j);
     }
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) step(c + 32 * j, g[j], v[j]);
   }
   for (; c < HV; c += 32) {
     Words<kIn> v{};
-    if (DOT) v = load_words<kIn>(ys, at + c);
+    if (DOT) v = load_stream<kIn>(ys, at + c);
     step(c, load_words<kOut>(dy, from + c), v);
   }
   if (DOT) {

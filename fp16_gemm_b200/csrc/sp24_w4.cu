@@ -8,91 +8,174 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 
-__device__ __forceinline__ float scale16(const uint16_t* s, int64_t i, int dtype) {
-  return dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(s[i]) : W4Half<SP24_F16>::get(s[i]);
-}
-
 // ------------------------------------------------------------------ quantise
 
-// Eight entries per thread (one 16-byte load, one code word), G / 8 neighbouring lanes per group.
+template <int DT>
+struct Pair16;
+template <>
+struct Pair16<SP24_BF16> {
+  using T = __nv_bfloat162;
+  static constexpr uint32_t kMagic = 0x43004300u;  // 2^7: its last place is 1
+};
+template <>
+struct Pair16<SP24_F16> {
+  using T = __half2;
+  static constexpr uint32_t kMagic = 0x64006400u;  // 2^10
+};
+template <int DT>
+__device__ __forceinline__ typename Pair16<DT>::T as_pair(uint32_t w) {
+  return reinterpret_cast<const typename Pair16<DT>::T&>(w);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pair_bits(T v) {
+  return reinterpret_cast<const uint32_t&>(v);
+}
+
+// G / 16 neighbouring lanes per group, sixteen entries each: two 16-byte loads, two code words.
 //
 // Why a reciprocal is enough: w and s are 16-bit floats with significands below 2^11, and |w| >= s/2
 // where a border matters, so |2w - (2n + 1) s| is 0 or at least s's last place: a quotient w / s that
-// is not exactly on a border n + 1/2 is at least 2^-12 away from it.  fma(w, 1/s, 1/2) is within
-// 2^-18 of w / s + 1/2 (|w / s| < 32), so with 2^-16 added its floor is that of the exact value, and
-// an exact border goes up.
-template <int DT>
-__global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* __restrict__ w, int64_t vecs, int group,
-                                                          int with_zeros, uint32_t* __restrict__ codes,
-                                                          uint16_t* __restrict__ scales, uint8_t* __restrict__ zeros) {
-  const int span = group / 8;  // lanes per group: 4, 8 or 16
-  for (int64_t base = (int64_t)blockIdx.x * 256; base < vecs; base += (int64_t)gridDim.x * 256) {
-    const int64_t i = base + threadIdx.x;
-    const uint4 x = i < vecs ? ldg_stream16(w + i) : make_uint4(0, 0, 0, 0);
-    const uint32_t word[4] = {x.x, x.y, x.z, x.w};
-    float v[8];
-    float lo = 0.0f, hi = 0.0f;
+// is not exactly on a border n + 1/2 is at least 2^-12 away from it.  The code is taken as the
+// nearest integer to 15 clamp(w / (15 s) + (z + 2^-16) / 15, 0, 1), which is within 2^-17 of
+// clamp(w / s + z + 2^-16, 0, 15): so it is that of the exact value, and an exact border goes up.
+//
+// Bound by instruction issue before HBM if done plainly, so the arithmetic is cut to four
+// instructions an entry: unpacking, one saturating fma (the clamp is its saturation), one fma that
+// adds 1.5 * 2^23 (whose last place is 1, which rounds to the integer), and one integer
+// multiply-add that joins the codes with the constant's bits still in them; their sum is
+// subtracted from the word at the end.  A scale above 2^100, whose 1 / (15 s) may be subnormal,
+// first has w and itself divided by 2^64.
+template <int DT, int G, bool ZEROS>
+__global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* __restrict__ w, int64_t groups,
+                                                          uint32_t* __restrict__ codes, uint16_t* __restrict__ scales,
+                                                          uint8_t* __restrict__ zeros) {
+  constexpr int L = G / 16;
+  using P = typename Pair16<DT>::T;
+  const int lane = threadIdx.x % L;
+  const int64_t step = (int64_t)gridDim.x * (256 / L);
+  // every lane of a group is in range together; those of other groups in the warp may not be
+  for (int64_t group = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; group < (groups + 31) / 32 * 32; group += step) {
+    const bool live = group < groups;
+    const int64_t at = group * (2 * L) + lane;
+    uint4 x[2] = {};
+    if (live) {
+      x[0] = ldg_stream16(w + at);
+      x[1] = ldg_stream16(w + at + L);
+    }
+    const uint32_t word[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    float lo = 0.0f, hi = 0.0f;  // symmetric: hi is the largest magnitude
+    if (ZEROS) {
+      P a = as_pair<DT>(word[0]), b = a;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = W4Half<DT>::get(word[k] & 0xffffu);
-      v[2 * k + 1] = W4Half<DT>::get(word[k] >> 16);
-    }
+      for (int k = 1; k < 8; ++k) {
+        a = __hmax2(a, as_pair<DT>(word[k]));
+        b = __hmin2(b, as_pair<DT>(word[k]));
+      }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      lo = fminf(lo, v[k]);
-      hi = fmaxf(hi, v[k]);
+      for (int d = 1; d < L; d <<= 1) {
+        a = __hmax2(a, as_pair<DT>(__shfl_xor_sync(kFull, pair_bits(a), d)));
+        b = __hmin2(b, as_pair<DT>(__shfl_xor_sync(kFull, pair_bits(b), d)));
+      }
+      const uint32_t ab = pair_bits(a), bb = pair_bits(b);
+      hi = fmaxf(0.0f, fmaxf(W4Half<DT>::get(ab & 0xffffu), W4Half<DT>::get(ab >> 16)));
+      lo = fminf(0.0f, fminf(W4Half<DT>::get(bb & 0xffffu), W4Half<DT>::get(bb >> 16)));
+    } else {
+      P a = __habs2(as_pair<DT>(word[0]));
+#pragma unroll
+      for (int k = 1; k < 8; ++k) a = __hmax2(a, __habs2(as_pair<DT>(word[k])));
+#pragma unroll
+      for (int d = 1; d < L; d <<= 1) a = __hmax2(a, as_pair<DT>(__shfl_xor_sync(kFull, pair_bits(a), d)));
+      const uint32_t ab = pair_bits(a);
+      hi = fmaxf(W4Half<DT>::get(ab & 0xffffu), W4Half<DT>::get(ab >> 16));
     }
-    for (int d = span / 2; d; d >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(kFull, lo, d));
-      hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, d));
-    }
-    const float width = with_zeros ? __fdiv_rn(hi - lo, 15.0f) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
-    uint32_t s16 = W4Half<DT>::put(width);
+    uint32_t s16 = W4Half<DT>::put(ZEROS ? __fdiv_rn(hi - lo, 15.0f) : __fdiv_rn(hi, 7.0f));
     float s = W4Half<DT>::get(s16);
     if (!(s >= 0x1p-126f)) s16 = 0, s = 0.0f;
-    const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-    constexpr float kHalf = 0.5f + 0x1p-16f;
+    const float down = s > 0x1p100f ? 0x1p-64f : 1.0f;
+    const float inv = s > 0.0f ? __fdiv_rn(1.0f / 15.0f, s * down) : 0.0f;  // 1 / (15 s) within 2^-23
+    constexpr float kMagic = 12582912.0f, kRoom = 0x1p-16f;
     float z = 8.0f;
-    if (with_zeros) z = s > 0.0f ? fminf(fmaxf(floorf(fmaf(-lo, inv, kHalf)), 0.0f), 15.0f) : 0.0f;
-    uint32_t out = 0;
+    // as with the codes: -lo / s, which is at most 15
+    if (ZEROS) z = s > 0.0f ? fmaf(__saturatef(fmaf(-lo * down, inv, kRoom / 15.0f)), 15.0f, kMagic) - kMagic : 0.0f;
+    const float shift = (z + kRoom) * (1.0f / 15.0f);
+    uint32_t out[2];
+    float scaled[16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float q = fminf(fmaxf(floorf(fmaf(v[k], inv, kHalf)) + z, 0.0f), 15.0f);
-      out |= (uint32_t)(int)q << (4 * k);
+      scaled[2 * k] = W4Half<DT>::get(word[k] & 0xffffu);
+      scaled[2 * k + 1] = W4Half<DT>::get(word[k] >> 16);
     }
-    if (i < vecs) {
-      codes[i] = out;
-      if (threadIdx.x % span == 0) {
-        scales[i / span] = (uint16_t)s16;
-        if (with_zeros) zeros[i / span] = (uint8_t)(int)z;
+    if (down != 1.0f)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) scaled[k] *= down;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int k = 7; k >= 0; --k)
+        sum = sum * 16 + __float_as_uint(fmaf(__saturatef(fmaf(scaled[8 * h + k], inv, shift)), 15.0f, kMagic));
+      out[h] = sum - 0x4b400000u * 0x11111111u;
+    }
+    if (live) {
+      codes[at] = out[0];
+      codes[at + L] = out[1];
+      if (lane == 0) {
+        scales[group] = (uint16_t)s16;
+        if (ZEROS) zeros[group] = (uint8_t)(int)z;
       }
     }
   }
 }
 
-template <int DT>
+// Eight codes per thread and turn, four turns in flight.  Where the output has the scales' type, q - z
+// (exact) times s is one multiplication in that type, which rounds once.
+template <int DT, int ST>
 __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __restrict__ codes,
-                                                            const uint16_t* __restrict__ scales, int scale_dtype,
-                                                            const uint8_t* __restrict__ zeros, int64_t vecs, int group,
-                                                            void* __restrict__ out) {
-  const int span = group / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += (int64_t)gridDim.x * 256) {
-    const uint32_t c = codes[i];
-    const float s = scale16(scales, i / span, scale_dtype);
-    const int z = zeros ? zeros[i / span] & 15 : 8;
-    float v[8];
+                                                            const uint16_t* __restrict__ scales,
+                                                            const uint8_t* __restrict__ zeros, int64_t vecs,
+                                                            int span_log, void* __restrict__ out) {
+  constexpr int kTurns = 4;
+  for (int64_t base = (int64_t)blockIdx.x * (256 * kTurns) + threadIdx.x; base < vecs;
+       base += (int64_t)gridDim.x * (256 * kTurns)) {
+    uint32_t c[kTurns], s16[kTurns], z[kTurns];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = (float)((int)(c >> (4 * k) & 15) - z) * s;
-    if (DT == SP24_F32) {
-      float4* o = reinterpret_cast<float4*>(out) + 2 * i;
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      constexpr int D = DT == SP24_F32 ? SP24_F16 : DT;
-      uint32_t p[4];
+    for (int k = 0; k < kTurns; ++k) {
+      const int64_t i = min(base + 256 * k, vecs - 1);
+      c[k] = __ldcs(codes + i);
+      s16[k] = scales[i >> span_log];
+      z[k] = zeros ? zeros[i >> span_log] & 15u : 8u;
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = W4Half<D>::put(v[2 * k]) | W4Half<D>::put(v[2 * k + 1]) << 16;
-      reinterpret_cast<uint4*>(out)[i] = make_uint4(p[0], p[1], p[2], p[3]);
+    for (int k = 0; k < kTurns; ++k) {
+      const int64_t i = base + 256 * k;
+      if (i >= vecs) break;
+      if constexpr (DT == ST) {
+        using P = typename Pair16<DT>::T;
+        const P zero = as_pair<DT>(Pair16<DT>::kMagic + z[k] * 0x10001u), scale = as_pair<DT>(s16[k] * 0x10001u);
+        uint32_t v[4];  // entries (0, 4), (1, 5), (2, 6), (3, 7)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = pair_bits(__hmul2(__hsub2(as_pair<DT>((c[k] >> (4 * j) & 0x000f000fu) | Pair16<DT>::kMagic), zero), scale));
+        __stcs(reinterpret_cast<uint4*>(out) + i,
+               make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                          __byte_perm(v[2], v[3], 0x7632)));
+      } else {
+        const float s = W4Half<ST>::get(s16[k]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = (__uint_as_float((c[k] >> (4 * j) & 15u) | 0x4b000000u) - (8388608.0f + (float)z[k])) * s;
+        if constexpr (DT == SP24_F32) {
+          float4* o = reinterpret_cast<float4*>(out) + 2 * i;
+          __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+          __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+        } else {
+          uint32_t p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = W4Half<DT>::put(v[2 * j]) | W4Half<DT>::put(v[2 * j + 1]) << 16;
+          __stcs(reinterpret_cast<uint4*>(out) + i, make_uint4(p[0], p[1], p[2], p[3]));
+        }
+      }
     }
   }
 }
@@ -127,9 +210,45 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   return x_dtype == SP24_BF16 ? gemv_w4_bf16(p, s) : gemv_w4_f16(p, s);
 }
 
-unsigned stream_ctas(int64_t vecs) {
-  const int64_t need = (vecs + 255) / 256, cap = (int64_t)sm_count() * 8;
+unsigned stream_ctas(int64_t need) {
+  const int64_t cap = (int64_t)sm_count() * 32;
   return (unsigned)(need < cap ? need : cap);
+}
+
+template <int DT, int G>
+int quantize(const void* w, int64_t groups, bool with_zeros, uint8_t* codes, void* scales, uint8_t* zeros,
+             cudaStream_t s) {
+  const unsigned ctas = stream_ctas((groups * (G / 16) + 255) / 256);
+  if (with_zeros)
+    quantize_w4_kernel<DT, G, true><<<ctas, 256, 0, s>>>(reinterpret_cast<const uint4*>(w), groups,
+                                                         reinterpret_cast<uint32_t*>(codes),
+                                                         reinterpret_cast<uint16_t*>(scales), zeros);
+  else
+    quantize_w4_kernel<DT, G, false><<<ctas, 256, 0, s>>>(reinterpret_cast<const uint4*>(w), groups,
+                                                          reinterpret_cast<uint32_t*>(codes),
+                                                          reinterpret_cast<uint16_t*>(scales), nullptr);
+  return launch_status();
+}
+
+template <int DT>
+int quantize_by_group(int group, const void* w, int64_t entries, bool with_zeros, uint8_t* codes, void* scales,
+                      uint8_t* zeros, cudaStream_t s) {
+  if (group == 128) return quantize<DT, 128>(w, entries / 128, with_zeros, codes, scales, zeros, s);
+  if (group == 64) return quantize<DT, 64>(w, entries / 64, with_zeros, codes, scales, zeros, s);
+  return quantize<DT, 32>(w, entries / 32, with_zeros, codes, scales, zeros, s);
+}
+
+template <int DT>
+int dequantize(const sp24_w4_operand* w, int64_t vecs, void* out, cudaStream_t s) {
+  const unsigned ctas = stream_ctas((vecs + 1023) / 1024);
+  const uint32_t* c = reinterpret_cast<const uint32_t*>(w->codes);
+  const uint16_t* sc = reinterpret_cast<const uint16_t*>(w->scales);
+  const int span_log = w->group == 128 ? 4 : w->group == 64 ? 3 : 2;
+  if (w->scale_dtype == SP24_BF16)
+    dequantize_w4_kernel<DT, SP24_BF16><<<ctas, 256, 0, s>>>(c, sc, w->zeros, vecs, span_log, out);
+  else
+    dequantize_w4_kernel<DT, SP24_F16><<<ctas, 256, 0, s>>>(c, sc, w->zeros, vecs, span_log, out);
+  return launch_status();
 }
 
 }  // namespace
@@ -146,16 +265,9 @@ extern "C" int sp24_quantize_w4(const void* w, int dtype, int64_t rows, int64_t 
   if (rows == 0 || K == 0) return SP24_OK;
   if (!w || !codes || !scales) return SP24_ERR_INVALID_ARG;
   if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(zeros, 4)) return SP24_ERR_ALIGN;
-  const int64_t vecs = rows * (K / 8);
-  if (dtype == SP24_BF16)
-    quantize_w4_kernel<SP24_BF16><<<stream_ctas(vecs), 256, 0, as_stream(stream)>>>(
-        reinterpret_cast<const uint4*>(w), vecs, group, with_zeros, reinterpret_cast<uint32_t*>(codes),
-        reinterpret_cast<uint16_t*>(scales), zeros);
-  else
-    quantize_w4_kernel<SP24_F16><<<stream_ctas(vecs), 256, 0, as_stream(stream)>>>(
-        reinterpret_cast<const uint4*>(w), vecs, group, with_zeros, reinterpret_cast<uint32_t*>(codes),
-        reinterpret_cast<uint16_t*>(scales), zeros);
-  return launch_status();
+  return dtype == SP24_BF16
+             ? quantize_by_group<SP24_BF16>(group, w, rows * K, with_zeros, codes, scales, zeros, as_stream(stream))
+             : quantize_by_group<SP24_F16>(group, w, rows * K, with_zeros, codes, scales, zeros, as_stream(stream));
 }
 
 extern "C" int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_t K, int out_dtype, void* out,
@@ -168,17 +280,9 @@ extern "C" int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_
   if (!w->codes || !w->scales || !out) return SP24_ERR_INVALID_ARG;
   if (!aligned(w->codes, 16) || !aligned(w->scales, 4) || !aligned(w->zeros, 4) || !aligned(out, 16)) return SP24_ERR_ALIGN;
   const int64_t vecs = rows * (K / 8);
-  const unsigned ctas = stream_ctas(vecs);
-  const uint32_t* c = reinterpret_cast<const uint32_t*>(w->codes);
-  const uint16_t* sc = reinterpret_cast<const uint16_t*>(w->scales);
-  cudaStream_t s = as_stream(stream);
-  if (out_dtype == SP24_F32)
-    dequantize_w4_kernel<SP24_F32><<<ctas, 256, 0, s>>>(c, sc, w->scale_dtype, w->zeros, vecs, w->group, out);
-  else if (out_dtype == SP24_BF16)
-    dequantize_w4_kernel<SP24_BF16><<<ctas, 256, 0, s>>>(c, sc, w->scale_dtype, w->zeros, vecs, w->group, out);
-  else
-    dequantize_w4_kernel<SP24_F16><<<ctas, 256, 0, s>>>(c, sc, w->scale_dtype, w->zeros, vecs, w->group, out);
-  return launch_status();
+  if (out_dtype == SP24_F32) return dequantize<SP24_F32>(w, vecs, out, as_stream(stream));
+  if (out_dtype == SP24_BF16) return dequantize<SP24_BF16>(w, vecs, out, as_stream(stream));
+  return dequantize<SP24_F16>(w, vecs, out, as_stream(stream));
 }
 
 extern "C" int sp24_gemv_w4(const void* x, int x_dtype, const sp24_w4_operand* w, int64_t M, int64_t N, int64_t K,

@@ -2,9 +2,15 @@
 // gradient of the logits ([P1] "Concurrency, not sparsity, is the lever" names the routed model;
 // the formulas are in sp24.h).
 //
-// One warp per token; lane l holds the logits l, l + 32, l + 64, ... of its row in registers.
-// Selection works on the values mapped to unsigned integers of the same order, so that a round is
-// one warp-wide integer maximum (the value) and one minimum (the lowest index that has it).
+// One warp per token; lane l holds the logits l, l + 32, l + 64, ... of its row in registers, and works
+// on them mapped to unsigned integers of the same order.
+//
+// Selection.  The topk-th largest of the 32 lanes' maxima is a floor under the topk largest logits
+// (that many lanes have one at or above it).  The few logits at or above the floor, 32 at most, are
+// gathered in shared memory and ranked against each other; that costs about a third of topk rounds
+// of "largest one left, take it away" (T = 4096, E = 512, topk = 10: 5.4 against 9.0 us), which remain
+// for rows whose ties leave more than 32, and for E <= 64, where a round is cheap (T = 16384, E = 64,
+// topk = 8: 7.8 against 8.6 us).
 #include "sp24_internal.cuh"
 
 namespace sp24 {
@@ -78,26 +84,74 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const void* __rest
     for (int j = 0; j < NV; ++j) total += expf(raw[j] - m);
     total = warp_sum(total);
   }
-  // topk rounds; lane s keeps slot s
+  // lane s is to keep slot s
   uint32_t mine = 0;
   int mine_id = -1;
-  for (int s = 0; s < topk; ++s) {
-    const uint32_t top = __reduce_max_sync(kFull, best);
-    if (top <= kKeyNegInf) break;
-    int at = INT32_MAX;
+  bool gathered = false;
+  if constexpr (NV > 2) {
+    uint32_t floor_key = best;
 #pragma unroll
-    for (int j = NV - 1; j >= 0; --j)
-      if (key[j] == top) at = lane + 32 * j;
-    at = __reduce_min_sync(kFull, at);
-    if (lane == s) {
-      mine = top;
-      mine_id = at;
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+      for (int d = size / 2; d; d /= 2) {  // bitonic, largest first
+        const uint32_t other = __shfl_xor_sync(kFull, floor_key, d);
+        const bool upper = (lane & d) != 0, rising = (lane & size) != 0 && size < 32;
+        floor_key = upper == rising ? max(floor_key, other) : min(floor_key, other);
+      }
+    floor_key = max(__shfl_sync(kFull, floor_key, topk - 1), kKeyNegInf + 1);
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) count += key[j] >= floor_key;
+    const int total_count = __reduce_add_sync(kFull, count);
+    __shared__ uint2 table[kThreads / 32][2][32];
+    gathered = total_count <= 32;
+    if (gathered) {
+      uint2* const found = table[threadIdx.x >> 5][0];
+      uint2* const ranked = table[threadIdx.x >> 5][1];
+      int at = count;  // exclusive sum over the lanes
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kFull, at, d);
+        if (lane >= d) at += o;
+      }
+      at -= count;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (key[j] >= floor_key) found[at++] = make_uint2(key[j], lane + 32 * j);
+      __syncwarp();
+      const uint2 own = lane < total_count ? found[lane] : make_uint2(0, 0);
+      int rank = 0;
+      for (int i = 0; i < total_count; ++i) {
+        const uint2 other = found[i];
+        rank += other.x > own.x || (other.x == own.x && other.y < own.y);
+      }
+      if (lane < total_count) ranked[rank] = own;
+      __syncwarp();
+      if (lane < min(total_count, topk)) {
+        mine = ranked[lane].x;
+        mine_id = (int)ranked[lane].y;
+      }
     }
-    best = 0;
+  }
+  if (!gathered) {
+    for (int s = 0; s < topk; ++s) {
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      if (top <= kKeyNegInf) break;
+      int at = INT32_MAX;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (at == lane + 32 * j) key[j] = 0;
-      best = max(best, key[j]);
+      for (int j = NV - 1; j >= 0; --j)
+        if (key[j] == top) at = lane + 32 * j;
+      at = __reduce_min_sync(kFull, at);
+      if (lane == s) {
+        mine = top;
+        mine_id = at;
+      }
+      best = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (at == lane + 32 * j) key[j] = 0;
+        best = max(best, key[j]);
+      }
     }
   }
   const bool live = mine_id >= 0;

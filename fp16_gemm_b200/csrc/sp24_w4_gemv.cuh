@@ -17,11 +17,13 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
 }
-// The four bytes at byte `at` (a multiple of 4) of an array of `total` bytes; zeros past its end.
-__device__ __forceinline__ void copy4(uint32_t dst, const void* base, int64_t at, int64_t total) {
-  const int n = at + 4 <= total ? 4 : at < total ? (int)(total - at) : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst),
-               "l"(reinterpret_cast<const uint8_t*>(base) + (n ? at : 0)), "r"(n));
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src));
+}
+// The part of the four bytes that lies before `end`, zeros for the rest; `base` is the array's start.
+__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src, const uint8_t* end, const uint8_t* base) {
+  const int n = src + 4 <= end ? 4 : src < end ? (int)(end - src) : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(n ? src : base), "r"(n));
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;"); }
 template <int N>
@@ -45,6 +47,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same on top of zero.
+template <int XT>
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (XT == SP24_BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // The code q as a 16-bit float without a conversion: its four bits are or-ed into the significand of
@@ -250,12 +267,22 @@ struct GemvKernel {
     // ---- fetching: chunk load_c of the item `load`.  Lane l copies piece l & 7 of rows (l >> 3) + 4 h.
     int load_c = kw;
     const uint8_t* code_src[MT][4];
-    const int64_t groups_total = p.E * p.N * KG;
     constexpr int kScaleOps = (16 * MT * kScaleWords + 31) / 32, kZeroOps = (16 * MT * kZeroWords + 31) / 32;
-    int64_t scale_group[kScaleOps], zero_group[kZeroOps ? kZeroOps : 1];  // first group of the row a word belongs to
-    auto aim = [&]() {  // the sources of a new item
+    // The words of scales and zero points this lane copies: 0 bytes for one that its row does not touch.
+    // A chunk has an even number of groups, so a row's scales keep their place within a word; its
+    // zero points keep theirs, or (two groups per chunk) move on by two bytes: hence zero_first.
+    const uint8_t* scale_src[kScaleOps];
+    bool scale_on[kScaleOps];
+    int64_t zero_first[kZeroOps ? kZeroOps : 1];
+    const int64_t groups_total = p.E * p.N * KG;
+    const uint8_t* const scales = reinterpret_cast<const uint8_t*>(p.scales);
+    const uint8_t* const scales_end = scales + 2 * groups_total;
+    bool near_end = false;  // a copied word may reach past the arrays' ends
+    auto aim = [&]() {      // the sources of a new item
       const int left = (int)min((int64_t)kCols, cols - (int64_t)load.col * kCols);  // columns of this item
       const int64_t row0 = load.tok.e * p.N + (int64_t)load.col * kCols;
+      // a row's last chunk may name up to seven groups too many, of as many further rows
+      near_end = row0 + (SWIGLU ? cols : 0) + kCols + 8 >= p.E * p.N;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         // rows past the end repeat the last one; they are computed and not stored
@@ -263,50 +290,56 @@ struct GemvKernel {
         const uint8_t* const src = p.codes + base * (K / 2) + (16 * (lane & 7) + kw * (kChunk / 2));
 #pragma unroll
         for (int h = 0; h < 4; ++h)
-          code_src[i][h] = src + (int64_t)min((SWIGLU ? 0 : 16 * i) + (lane >> 3) + 4 * h, left - 1) * (K / 2);
+          code_src[i][h] = src + (uint32_t)(min((SWIGLU ? 0 : 16 * i) + (lane >> 3) + 4 * h, left - 1) * (K / 2));
       }
       auto first_group = [&](int r) {
-        return (row0 + (SWIGLU ? (r >> 4) * cols : 0) + min(SWIGLU ? r & 15 : r, left - 1)) * KG + kw * kGroups;
+        return (row0 + (SWIGLU ? (r >> 4) * cols : 0)) * KG + (min(SWIGLU ? r & 15 : r, left - 1) * KG + kw * kGroups);
       };
 #pragma unroll
-      for (int i = 0; i < kScaleOps; ++i) scale_group[i] = first_group((lane + 32 * i) / kScaleWords & (16 * MT - 1));
+      for (int i = 0; i < kScaleOps; ++i) {
+        const int s = lane + 32 * i, w = s % kScaleWords;
+        const int64_t at = first_group(s / kScaleWords & (16 * MT - 1));
+        scale_on[i] = s < 16 * MT * kScaleWords && 2 * w < ((int)at & 1) + kGroups;
+        scale_src[i] = scales + (at >> 1) * 4 + 4 * w;
+      }
 #pragma unroll
       for (int i = 0; i < kZeroOps; ++i)
-        zero_group[i] = first_group((lane + 32 * i) / (ZEROS ? kZeroWords : 1) & (16 * MT - 1));
+        zero_first[i] = first_group((lane + 32 * i) / (ZEROS ? kZeroWords : 1) & (16 * MT - 1));
     };
-    // rows r, r + 8 swizzle alike; a row's pieces (16 bytes) change places by its number
-    const uint32_t code_dst = ring_at + (lane >> 3) * 128;
-    auto fetch = [&](int slot) {
+    const uint32_t code_dst = ring_at + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));  // h odd: ^ 64
+    auto fetch = [&](uint32_t stage) {
       if (load.left > 0) {
-        const uint32_t dst = code_dst + slot * kStage;
+        const uint32_t dst = code_dst + stage;
         if (load_c * kChunk + 32 * (lane & 7) < K) {
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-              copy16(dst + i * kTileBytes + h * 512 + 16 * ((lane & 7) ^ ((lane >> 3) + 4 * (h & 1))), code_src[i][h]);
+            for (int h = 0; h < 4; ++h) copy16((h & 1 ? dst ^ 64 : dst) + (i * kTileBytes + h * 512), code_src[i][h]);
         }
-        const uint32_t table = ring_at + slot * kStage + MT * kTileBytes;
+        const uint32_t table = ring_at + stage + MT * kTileBytes;
+        if (!near_end) {
 #pragma unroll
-        for (int i = 0; i < kScaleOps; ++i) {
-          const int s = lane + 32 * i, w = s % kScaleWords;
-          const int64_t at = scale_group[i];
-          if (s < 16 * MT * kScaleWords && 2 * w < ((int)at & 1) + kGroups)
-            copy4(table + 4 * s, p.scales, (at >> 1) * 4 + 4 * w, 2 * groups_total);
-          scale_group[i] += wk * kGroups;
+          for (int i = 0; i < kScaleOps; ++i)
+            if (scale_on[i]) copy4(table + 4 * (lane + 32 * i), scale_src[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kScaleOps; ++i)
+            if (scale_on[i]) copy4(table + 4 * (lane + 32 * i), scale_src[i], scales_end, scales);
         }
 #pragma unroll
         for (int i = 0; i < kZeroOps; ++i) {
           const int s = lane + 32 * i, w = s % (ZEROS ? kZeroWords : 1);
-          const int64_t at = zero_group[i];
+          const int64_t at = zero_first[i];
           if (s < 16 * MT * kZeroWords && 4 * w < ((int)at & 3) + kGroups)
-            copy4(table + kZeroAt + 4 * s, p.zeros, (at >> 2) * 4 + 4 * w, groups_total);
-          zero_group[i] += wk * kGroups;
+            copy4(table + kZeroAt + 4 * s, p.zeros + ((at >> 2) * 4 + 4 * w), p.zeros + groups_total, p.zeros);
+          zero_first[i] += wk * kGroups;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int h = 0; h < 4; ++h) code_src[i][h] += wk * (kChunk / 2);
+#pragma unroll
+        for (int i = 0; i < kScaleOps; ++i) scale_src[i] += wk * (2 * kGroups);
         load_c += wk;
         if (load_c >= chunks) {
           load.advance(p, col_tiles, teams);
@@ -319,7 +352,7 @@ struct GemvKernel {
 
     if (load.left > 0) aim();
 #pragma unroll
-    for (int s = 0; s < S; ++s) fetch(s);
+    for (int s = 0; s < S; ++s) fetch(s * kStage);
     if (XW) {
       const int pieces = K / 8;
       for (int m = 0; m < (int)p.M; ++m)
@@ -342,9 +375,9 @@ struct GemvKernel {
 #pragma unroll
         for (int k = 0; k < 4; ++k) tot[i][n][k] = 0.0f;
 
-    // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4)
+    // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4); block j + 2 n: ^ 32 n
     const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
-    const uint32_t lm_at = ring_at + lm_row * 128;
+    const uint32_t lm_at = ring_at + lm_row * 128 + 16 * ((lane >> 4) ^ (lane & 7));
     const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
     int group_row[MT];         // (this lane's row of tile i) * KG, as far as its place within a word goes
     auto aim_use = [&]() {
@@ -374,19 +407,20 @@ struct GemvKernel {
                           : __ldg(reinterpret_cast<const uint4*>(x_row[n] + (int64_t)c * (2 * kChunk) + 64 * (4 * half + j)));
     };
     // blocks j, j + 1 of the chunk
-    auto multiply2 = [&](int slot, int c, int j, const uint4 (&x0)[NT], const uint4 (&x1)[NT], bool both) {
-      const uint8_t* const table = ring + slot * kStage + MT * kTileBytes;
+    auto multiply2 = [&](uint32_t stage, int c, int j, const uint4 (&x0)[NT], const uint4 (&x1)[NT], bool both) {
+      const uint8_t* const table = ring + stage + MT * kTileBytes;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         uint32_t words[4];
-        ldmatrix4(words, lm_at + slot * kStage + i * kTileBytes + 16 * ((j + (lane >> 4)) ^ (lane & 7)));
+        ldmatrix4(words, (lm_at ^ (16 * j)) + stage + i * kTileBytes);
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
           if (jb && !both) break;
           const int jj = j + jb;
           uint32_t zl = kMagic<XT> + 0x80008u, zh = zl;
-          const int first = group_row[i] + c * kGroups;  // rows g and g + 8 start alike within a word
+          // rows g and g + 8 start alike within a word
           if (ZEROS) {
+            const int first = group_row[i] + c * kGroups;
             const uint8_t* zp = table + kZeroAt + (16 * i + g) * kZeroWords * 4 + (first & 3) + jj / GB;
             zl = kMagic<XT> + (zp[0] & 15u) * 0x10001u;
             zh = kMagic<XT> + (zp[8 * kZeroWords * 4] & 15u) * 0x10001u;
@@ -401,15 +435,14 @@ struct GemvKernel {
             if (!XW)
               b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
                              __byte_perm(b.y, b.w, 0x7632));
-            if (jj % GB == 0) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) acc[i][n][k] = 0.0f;
-            }
-            mma16816<XT>(acc[i][n], a0, b.x, b.y);
+            if (jj % GB == 0)
+              mma16816_first<XT>(acc[i][n], a0, b.x, b.y);
+            else
+              mma16816<XT>(acc[i][n], a0, b.x, b.y);
             mma16816<XT>(acc[i][n], a1, b.z, b.w);
           }
           if ((jj + 1) % GB == 0) {
-            const uint8_t* sp = table + (16 * i + g) * kScaleWords * 4 + 2 * ((first & 1) + jj / GB);
+            const uint8_t* sp = table + (16 * i + g) * kScaleWords * 4 + 2 * ((group_row[i] & 1) + jj / GB);
             const uint32_t l = *reinterpret_cast<const uint16_t*>(sp);
             const uint32_t h = *reinterpret_cast<const uint16_t*>(sp + 8 * kScaleWords * 4);
             const float sl = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(l) : W4Half<SP24_F16>::get(l);
@@ -422,38 +455,39 @@ struct GemvKernel {
         }
       }
     };
-    auto multiply = [&](int slot, int c, int half, int blocks) {
+    auto multiply = [&](uint32_t stage, int c, int half, int blocks) {
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
         uint4 x0[NT], x1[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) x0[n] = xv[n][j], x1[n] = xv[n][j + 1];
-        if (4 * half + j < blocks) multiply2(slot, c, 4 * half + j, x0, x1, 4 * half + j + 1 < blocks);
+        if (4 * half + j < blocks) multiply2(stage, c, 4 * half + j, x0, x1, 4 * half + j + 1 < blocks);
       }
     };
 
-    int slot = 0, c = kw, buffer = 0;
+    uint32_t stage = 0;
+    int c = kw, buffer = 0;
     while (true) {
       const int blocks = min(kChunk / 32, K / 32 - kChunk / 32 * c);
       if (blocks == kChunk / 32) {  // a whole chunk: straight through
         read_x(c, 0, kChunk / 32);
         copy_wait<S - 1>();
         __syncwarp();
-        multiply(slot, c, 0, kChunk / 32);
+        multiply(stage, c, 0, kChunk / 32);
         read_x(c, 1, kChunk / 32);
-        multiply(slot, c, 1, kChunk / 32);
+        multiply(stage, c, 1, kChunk / 32);
       } else {
         copy_wait<S - 1>();
         __syncwarp();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           read_x(c, half, blocks);
-          multiply(slot, c, half, blocks);
+          multiply(stage, c, half, blocks);
         }
       }
       __syncwarp();
-      fetch(slot);
-      slot = slot + 1 == S ? 0 : slot + 1;
+      fetch(stage);
+      stage = stage == (S - 1) * kStage ? 0 : stage + kStage;
       c += wk;
       if (c < chunks) continue;
 
@@ -530,7 +564,7 @@ int launch_gemv(GemvW4 p, cudaStream_t s) {
   int64_t best = INT64_MAX;
   for (int k = 0; k <= kWarpsLog && (k == 0 || (1 << k) <= chunks); ++k) {
     const int64_t teams = (int64_t)sms << (kWarpsLog - k), rounds = (items + teams - 1) / teams;
-    const int64_t cost = rounds * ((chunks + (1 << k) - 1) >> k) * 2 + rounds;
+    const int64_t cost = rounds * (((chunks + (1 << k) - 1) >> k) * 10 + 7);
     if (cost < best) best = cost, p.wk_log = k;
   }
   const int64_t ctas = items < sms ? items : sms;

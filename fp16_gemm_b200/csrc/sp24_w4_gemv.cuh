@@ -245,7 +245,8 @@ struct GemvKernel {
   static int64_t smem_bytes(const GemvW4& p) { return kFixed + (XW ? p.M * x_stride((int)p.K) : 0); }
 
   static __device__ __forceinline__ void run(const GemvW4& p, uint8_t* smem) {
-    const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+    // a warp-wide reduction leaves its result where the compiler knows that all lanes agree
+    const int lane = threadIdx.x & 31, warp = (int)__reduce_max_sync(kFull, threadIdx.x >> 5);
     const int g = lane >> 2, t = lane & 3;
     const int wk = 1 << p.wk_log, kw = warp & (wk - 1), in_cta = warp >> p.wk_log;
     const int team = in_cta * gridDim.x + blockIdx.x, teams = gridDim.x << (kWarpsLog - p.wk_log);
@@ -395,9 +396,8 @@ struct GemvKernel {
     };
     aim_use();
 
-    uint4 xv[NT][4];
     // x of blocks 4 half .. 4 half + 3 of chunk c, as it stands in memory
-    auto read_x = [&](int c, int half, int blocks) {
+    auto read_x = [&](uint4 (&xv)[NT][4], int c, int half, int blocks) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -407,7 +407,7 @@ struct GemvKernel {
                           : __ldg(reinterpret_cast<const uint4*>(x_row[n] + (int64_t)c * (2 * kChunk) + 64 * (4 * half + j)));
     };
     // blocks j, j + 1 of the chunk
-    auto multiply2 = [&](uint32_t stage, int c, int j, const uint4 (&x0)[NT], const uint4 (&x1)[NT], bool both) {
+    auto multiply2 = [&](uint32_t stage, int c, int j, const uint4 (&xv)[NT][4], bool both) {
       const uint8_t* const table = ring + stage + MT * kTileBytes;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -431,7 +431,7 @@ struct GemvKernel {
           const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            uint4 b = jb ? x1[n] : x0[n];
+            uint4 b = xv[n][jj & 3];
             if (!XW)
               b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
                              __byte_perm(b.y, b.w, 0x7632));
@@ -455,14 +455,10 @@ struct GemvKernel {
         }
       }
     };
-    auto multiply = [&](uint32_t stage, int c, int half, int blocks) {
+    auto multiply = [&](uint32_t stage, int c, const uint4 (&xv)[NT][4], int half, int blocks) {
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        uint4 x0[NT], x1[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) x0[n] = xv[n][j], x1[n] = xv[n][j + 1];
-        if (4 * half + j < blocks) multiply2(stage, c, 4 * half + j, x0, x1, 4 * half + j + 1 < blocks);
-      }
+      for (int j = 4 * half; j < 4 * half + 4; j += 2)
+        if (j < blocks) multiply2(stage, c, j, xv, j + 1 < blocks);
     };
 
     uint32_t stage = 0;
@@ -470,20 +466,21 @@ struct GemvKernel {
     while (true) {
       const int blocks = min(kChunk / 32, K / 32 - kChunk / 32 * c);
       if (blocks == kChunk / 32) {  // a whole chunk: straight through
-        read_x(c, 0, kChunk / 32);
+        uint4 x0[NT][4], x1[NT][4];
+        read_x(x0, c, 0, kChunk / 32);
         copy_wait<S - 1>();
         __syncwarp();
-        multiply(stage, c, 0, kChunk / 32);
-        read_x(c, 1, kChunk / 32);
-        multiply(stage, c, 1, kChunk / 32);
+        multiply(stage, c, x0, 0, kChunk / 32);
+        read_x(x1, c, 1, kChunk / 32);
+        multiply(stage, c, x1, 1, kChunk / 32);
       } else {
         copy_wait<S - 1>();
         __syncwarp();
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          read_x(c, half, blocks);
-          multiply(stage, c, half, blocks);
-        }
+        uint4 x0[NT][4];
+        read_x(x0, c, 0, blocks);
+        multiply(stage, c, x0, 0, blocks);
+        read_x(x0, c, 1, blocks);
+        multiply(stage, c, x0, 1, blocks);
       }
       __syncwarp();
       fetch(stage);

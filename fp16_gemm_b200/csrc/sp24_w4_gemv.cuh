@@ -64,35 +64,54 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// The code q as a 16-bit float without a conversion: its four bits are or-ed into the significand of
-// 2^10 (f16) or 2^7 (bf16), whose last place is 1, and the same number plus the zero point is
-// subtracted: q - z exactly.  kMagic is that number's bits, in both halves of a word.
+// The code q as a 16-bit float without a conversion.  Bits below a float's exponent field, alone, are a
+// subnormal number, and the numbers up to twice the smallest normal one are evenly spaced: the four
+// bits of a code at the bottom of a 16-bit half are q times the smallest subnormal, those above them 16 q
+// times it (bf16: with the last exponent bit among them).  One fma by a power of two, which differs by
+// 16 between the two places, makes both (q - z) kUnit exactly, where kUnit is a power of two that
+// bf16's largest power of two allows; the sums are divided by it at the end.  So a word takes four
+// masks, one shift and four fmas.
 template <int XT>
-constexpr uint32_t kMagic = XT == SP24_BF16 ? 0x43004300u : 0x64006400u;
-
-// (word & mask) | magic, one three-input logic operation.
-__device__ __forceinline__ uint32_t and_or(uint32_t word, uint32_t mask, uint32_t magic) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(word), "r"(mask), "r"(magic));
-  return r;
-}
-
-template <int XT>
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-  if (XT == SP24_BF16) {
-    const __nv_bfloat162 r = __hsub2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(b));
+struct Expand;
+template <>
+struct Expand<SP24_BF16> {
+  static constexpr float kUnit = 0x1p-6f;
+  static constexpr uint32_t kLow = 0x7f007f00u, kHigh = 0x7d007d00u;  // 2^127 and 2^123 (smallest subnormal: 2^-133)
+  // -z kUnit in both halves, for z in 0..15: the bits of z as a float, its exponent moved
+  static __device__ __forceinline__ uint32_t zero(uint32_t z) {
+    const __nv_bfloat162 v = __float2bfloat162_rn((float)(int)z * -kUnit);
+    return reinterpret_cast<const uint32_t&>(v);
+  }
+  static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    const __nv_bfloat162 r = __hfma2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(b),
+                                     reinterpret_cast<const __nv_bfloat162&>(c));
     return reinterpret_cast<const uint32_t&>(r);
   }
-  const __half2 r = __hsub2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b));
-  return reinterpret_cast<const uint32_t&>(r);
-}
+};
+template <>
+struct Expand<SP24_F16> {
+  static constexpr float kUnit = 0x1p-10f;
+  static constexpr uint32_t kLow = 0x74007400u, kHigh = 0x64006400u;  // 2^14 and 2^10 (smallest subnormal: 2^-24)
+  static __device__ __forceinline__ uint32_t zero(uint32_t z) {
+    const __half2 v = __float2half2_rn((float)(int)z * -kUnit);
+    return reinterpret_cast<const uint32_t&>(v);
+  }
+  static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 r = __hfma2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b),
+                              reinterpret_cast<const __half2&>(c));
+    return reinterpret_cast<const uint32_t&>(r);
+  }
+};
 
-// The eight codes of a word as four pairs of q - z: entries (0, 4), (1, 5), (2, 6), (3, 7).  `zero` is
-// kMagic + z in both halves.
+// The eight codes of a word as four pairs of (q - z) kUnit: entries (0, 4), (1, 5), (2, 6), (3, 7).
 template <int XT>
 __device__ __forceinline__ void expand8(uint32_t word, uint32_t zero, uint32_t (&out)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) out[k] = sub2<XT>(and_or(word >> (4 * k), 0x000f000fu, kMagic<XT>), zero);
+  using X = Expand<XT>;
+  const uint32_t up = word >> 8;
+  out[0] = X::fma2(word & 0x000f000fu, X::kLow, zero);
+  out[1] = X::fma2(word & 0x00f000f0u, X::kHigh, zero);
+  out[2] = X::fma2(up & 0x000f000fu, X::kLow, zero);
+  out[3] = X::fma2(up & 0x00f000f0u, X::kHigh, zero);
 }
 
 // The token tiles of all experts, in expert order: expert e has ceil(rows of e / step) of them.
@@ -417,13 +436,13 @@ struct GemvKernel {
         for (int jb = 0; jb < 2; ++jb) {
           if (jb && !both) break;
           const int jj = j + jb;
-          uint32_t zl = kMagic<XT> + 0x80008u, zh = zl;
+          uint32_t zl = Expand<XT>::zero(8), zh = zl;
           // rows g and g + 8 start alike within a word
           if (ZEROS) {
             const int first = group_row[i] + c * kGroups;
             const uint8_t* zp = table + kZeroAt + (16 * i + g) * kZeroWords * 4 + (first & 3) + jj / GB;
-            zl = kMagic<XT> + (zp[0] & 15u) * 0x10001u;
-            zh = kMagic<XT> + (zp[8 * kZeroWords * 4] & 15u) * 0x10001u;
+            zl = Expand<XT>::zero(zp[0] & 15u);
+            zh = Expand<XT>::zero(zp[8 * kZeroWords * 4] & 15u);
           }
           uint32_t lo[4], hi[4];
           expand8<XT>(words[2 * jb], zl, lo);
@@ -498,7 +517,7 @@ struct GemvKernel {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int m = 8 * n + 2 * t + (k & 1);
-            if (m < rows) mine[(i * kTok + m) * 16 + g + 8 * (k >> 1)] = tot[i][n][k];
+            if (m < rows) mine[(i * kTok + m) * 16 + g + 8 * (k >> 1)] = tot[i][n][k] * (1.0f / Expand<XT>::kUnit);
             tot[i][n][k] = 0.0f;
           }
       if (wk == 1)

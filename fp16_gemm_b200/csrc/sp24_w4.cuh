@@ -28,7 +28,6 @@ struct GemvW4 {
   void* y;
   int64_t M, E, N, K;
   int scale_dtype, group, act, y_f32;
-  int wk_log;  // chosen by the launch: log2 of the warps that share an item's K
 };
 
 int gemv_w4_bf16(const GemvW4& p, cudaStream_t s);

@@ -1,15 +1,15 @@
 // The kernel of sp24_gemv_w4 / sp24_gemv_w4_grouped; each type of x is a translation unit of its own.
 #pragma once
 
+#include "sp24_tc.cuh"
 #include "sp24_w4.cuh"
 
 namespace sp24 {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kWarps = 16;
+constexpr int kTeams = 4, kMulPerTeam = 4, kMulWarps = kTeams * kMulPerTeam;
 constexpr int kChunk = 256;     // entries of K per stage: 128 code bytes of each row
-constexpr int kWarpsLog = 4;
 constexpr int kTileBytes = 16 * kChunk / 2;
 constexpr int kSmemMax = 232448;  // of one CTA
 
@@ -25,11 +25,11 @@ __device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src, const ui
   const int n = src + 4 <= end ? 4 : src < end ? (int)(end - src) : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(n ? src : base), "r"(n));
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N));
+// The barrier gets this thread's arrival when all its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -82,6 +82,10 @@ struct Expand<SP24_BF16> {
     const __nv_bfloat162 v = __float2bfloat162_rn((float)(int)z * -kUnit);
     return reinterpret_cast<const uint32_t&>(v);
   }
+  // the same from a byte whose low four bits are z
+  static __device__ __forceinline__ uint32_t zero_of(uint32_t byte) {
+    return fma2((byte & 15u) * 0x10001u, kLow | 0x80008000u, 0x80008000u);
+  }
   static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     const __nv_bfloat162 r = __hfma2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(b),
                                      reinterpret_cast<const __nv_bfloat162&>(c));
@@ -95,6 +99,9 @@ struct Expand<SP24_F16> {
   static __device__ __forceinline__ uint32_t zero(uint32_t z) {
     const __half2 v = __float2half2_rn((float)(int)z * -kUnit);
     return reinterpret_cast<const uint32_t&>(v);
+  }
+  static __device__ __forceinline__ uint32_t zero_of(uint32_t byte) {
+    return fma2((byte & 15u) * 0x10001u, kLow | 0x80008000u, 0x80008000u);
   }
   static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     const __half2 r = __hfma2(reinterpret_cast<const __half2&>(a), reinterpret_cast<const __half2&>(b),
@@ -233,30 +240,37 @@ struct Walk {
 // y = x W^T for up to 8 NT rows of x and MT tiles of 16 weight rows (with SwiGLU: a gate tile and its
 // up tile).  The weight rows are the MMA's M, the rows of x its N.
 //
-// Persistent, one CTA of 16 warps per SM.  2^wk_log warps are a team, which walks work items of its
-// own: K is split over them in chunks of 256 entries, each warp streaming its chunks of codes and
-// scales through a ring of S stages with cp.async that runs ahead across the items' borders; the
-// partial sums meet in shared memory in a fixed order, in two buffers that take turns, so one barrier
-// of the team per item is enough.  An ldmatrix of 16-byte row pieces hands lane (g, t) the eight
-// codes 8t .. 8t + 7 of a 32-entry block of rows g and g + 8; the MMA may sum K in any order, so the
-// pairs that expand8 gives are fed as they come, with x's pairs picked alike.  A group's sum is
-// scaled in fp32.
+// Persistent, one CTA per SM of four teams, each of which walks work items of its own: one warp
+// copies (cp.async, S stages of four chunks of 256 entries ahead, across the items' borders), four
+// multiply, each a chunk of every four along K; mbarriers tell the stages full and empty.  The
+// partial sums of the four meet in shared memory in a fixed order, in two buffers that take turns, so
+// one barrier of the team per item is enough.
+//
+// An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of a 32-entry block
+// of rows g and g + 8; the MMA may sum K in any order, so the pairs that expand8 gives are fed as
+// they come, with x's pairs picked alike.  A group's sum is scaled in fp32.
 //
 // XW: x stands in shared memory whole, its pairs picked when it is brought there; otherwise (experts,
 // or a large x) it is read from global memory half a chunk ahead and its pairs are picked at each use.
+//
+// Waits are bounded by the library's wait limit: a warp that gives up records it, does not wait again
+// and passes through the rest of its items, so every barrier is still met.
 template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
 struct GemvKernel {
   static constexpr int kTok = 8 * NT;
   static constexpr int kCols = SWIGLU ? 16 : 16 * MT;    // output columns of an item
   static constexpr int kGroups = kChunk / 32 / GB;       // groups per chunk
   // A chunk's scales of one row are 2 kGroups bytes at any even place, its zero points kGroups bytes
-  // at any place: the aligned words that they may touch are copied.
+  // at any place: the aligned words that they may touch are copied.  A chunk has an even number of
+  // groups, so a row's scales keep their place within a word from chunk to chunk.
   static constexpr int kScaleWords = kGroups / 2 + 1;
   static constexpr int kZeroWords = ZEROS ? (kGroups + 2) / 4 + 1 : 0;
   static constexpr int kZeroAt = 16 * MT * kScaleWords * 4;                     // in bytes, behind the scales
   static constexpr int kStage = MT * kTileBytes + (kZeroAt + 16 * MT * kZeroWords * 4 + 127) / 128 * 128;
   static constexpr int kPartial = MT * kTok * 16;                               // floats per warp and buffer
-  static constexpr int kFixed = 2 * kWarps * kPartial * 4 + kWarps * S * kStage;
+  static constexpr int kBarriers = 1024;                                        // bytes
+  static constexpr int kRing = kBarriers + 2 * kMulWarps * kPartial * 4;
+  static constexpr int kFixed = kRing + kMulWarps * S * kStage;
 
   static __host__ __device__ __forceinline__ int x_stride(int K) {
     return (2 * K + 127) / 128 * 128 + 64;  // two neighbouring rows of x never meet in a bank
@@ -265,56 +279,67 @@ struct GemvKernel {
 
   static __device__ __forceinline__ void run(const GemvW4& p, uint8_t* smem) {
     // a warp-wide reduction leaves its result where the compiler knows that all lanes agree
-    const int lane = threadIdx.x & 31, warp = (int)__reduce_max_sync(kFull, threadIdx.x >> 5);
-    const int g = lane >> 2, t = lane & 3;
-    const int wk = 1 << p.wk_log, kw = warp & (wk - 1), in_cta = warp >> p.wk_log;
-    const int team = in_cta * gridDim.x + blockIdx.x, teams = gridDim.x << (kWarpsLog - p.wk_log);
-    const int64_t cols = SWIGLU ? p.N / 2 : p.N;
-    const int col_tiles = (int)((cols + kCols - 1) / kCols);
+    const int warp = (int)__reduce_max_sync(kFull, threadIdx.x >> 5);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);  // [team][stage][full, empty]
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kTeams * S; ++i) {
+        tc::mbar_init(bars + 2 * i, 32);            // every lane of the copying warp
+        tc::mbar_init(bars + 2 * i + 1, kMulPerTeam);  // one lane of each multiplying warp
+      }
+      tc::fence_mbar_init();
+    }
+    __syncthreads();
+    const bool copies = warp >= kMulWarps;
+    const int in_cta = copies ? warp - kMulWarps : warp / kMulPerTeam;
+    const int team = in_cta * gridDim.x + blockIdx.x, teams = gridDim.x * kTeams;
+    uint8_t* const ring = smem + kRing + in_cta * (kMulPerTeam * S * kStage);  // [stage][chunk of the four]
+    if (copies)
+      copy(p, ring, bars + 2 * S * in_cta, team, teams);
+    else
+      multiply_all(p, smem, ring, bars + 2 * S * in_cta, warp, in_cta, team, teams);
+  }
+
+  static __device__ __forceinline__ int64_t columns(const GemvW4& p) { return SWIGLU ? p.N / 2 : p.N; }
+  static __device__ __forceinline__ int column_tiles(const GemvW4& p) {
+    return (int)((columns(p) + kCols - 1) / kCols);
+  }
+
+  // ---- the copying warp: lane l copies piece l & 7 of rows (l >> 3) + 4 h of each of the four chunks
+  static __device__ __forceinline__ void copy(const GemvW4& p, uint8_t* ring, uint64_t* bars, int team, int teams) {
+    const int lane = threadIdx.x & 31;
+    const int64_t cols = columns(p);
+    const int col_tiles = column_tiles(p);
     const int K = (int)p.K, KG = K / (32 * GB);
-    const int chunks = (K + kChunk - 1) / kChunk;
-
-    float* const partials = reinterpret_cast<float*>(smem);  // [buffer][warp][tile][token][row]
-    uint8_t* const ring = smem + 2 * kWarps * kPartial * 4 + warp * S * kStage;
-    uint8_t* const x_all = smem + kFixed;
-    const uint32_t ring_at = smem_addr(ring);
-
-    Walk<kTok> load, use;  // what is being fetched and what is being multiplied
-    load.left = 0;
-    if (team < teams) load.start(p, col_tiles, team, teams);
-    use = load;
-
-    // ---- fetching: chunk load_c of the item `load`.  Lane l copies piece l & 7 of rows (l >> 3) + 4 h.
-    int load_c = kw;
-    const uint8_t* code_src[MT][4];
-    constexpr int kScaleOps = (16 * MT * kScaleWords + 31) / 32, kZeroOps = (16 * MT * kZeroWords + 31) / 32;
-    // The words of scales and zero points this lane copies: 0 bytes for one that its row does not touch.
-    // A chunk has an even number of groups, so a row's scales keep their place within a word; its
-    // zero points keep theirs, or (two groups per chunk) move on by two bytes: hence zero_first.
-    const uint8_t* scale_src[kScaleOps];
-    bool scale_on[kScaleOps];
-    int64_t zero_first[kZeroOps ? kZeroOps : 1];
     const int64_t groups_total = p.E * p.N * KG;
     const uint8_t* const scales = reinterpret_cast<const uint8_t*>(p.scales);
-    const uint8_t* const scales_end = scales + 2 * groups_total;
-    bool near_end = false;  // a copied word may reach past the arrays' ends
-    auto aim = [&]() {      // the sources of a new item
-      const int left = (int)min((int64_t)kCols, cols - (int64_t)load.col * kCols);  // columns of this item
-      const int64_t row0 = load.tok.e * p.N + (int64_t)load.col * kCols;
-      // a row's last chunk may name up to seven groups too many, of as many further rows
-      near_end = row0 + (SWIGLU ? cols : 0) + kCols + 8 >= p.E * p.N;
+    const uint32_t ring_at = smem_addr(ring);
+    // a row's pieces change places by its number: row r's piece i stands at i ^ (r & 7)
+    const uint32_t code_at = ring_at + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));  // h odd: ^ 64
+    constexpr int kScaleOps = (16 * MT * kScaleWords + 31) / 32, kZeroOps = (16 * MT * kZeroWords + 31) / 32;
+    Walk<kTok> walk;
+    walk.start(p, col_tiles, team, teams);
+    int stage = 0, round = 0;
+    for (; walk.left > 0; walk.advance(p, col_tiles, teams)) {
+      const int left = (int)min((int64_t)kCols, cols - (int64_t)walk.col * kCols);  // columns of this item
+      const int64_t row0 = walk.tok.e * p.N + (int64_t)walk.col * kCols;
+      // a copied word may reach past the arrays' ends: a row's last chunk may name up to seven groups
+      // too many, of as many further rows
+      const bool near_end = row0 + (SWIGLU ? cols : 0) + kCols + 8 >= p.E * p.N;
+      // rows past the end repeat the last one; they are computed and not stored
+      const uint8_t* code_src[MT][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        // rows past the end repeat the last one; they are computed and not stored
-        const int64_t base = row0 + (SWIGLU ? i * cols : 0);
-        const uint8_t* const src = p.codes + base * (K / 2) + (16 * (lane & 7) + kw * (kChunk / 2));
+        const uint8_t* const src = p.codes + (row0 + (SWIGLU ? i * cols : 0)) * (K / 2) + 16 * (lane & 7);
 #pragma unroll
         for (int h = 0; h < 4; ++h)
           code_src[i][h] = src + (uint32_t)(min((SWIGLU ? 0 : 16 * i) + (lane >> 3) + 4 * h, left - 1) * (K / 2));
       }
       auto first_group = [&](int r) {
-        return (row0 + (SWIGLU ? (r >> 4) * cols : 0)) * KG + (min(SWIGLU ? r & 15 : r, left - 1) * KG + kw * kGroups);
+        return (row0 + (SWIGLU ? (r >> 4) * cols : 0)) * KG + min(SWIGLU ? r & 15 : r, left - 1) * KG;
       };
+      const uint8_t* scale_src[kScaleOps];
+      bool scale_on[kScaleOps];
+      int64_t zero_first[kZeroOps ? kZeroOps : 1];
 #pragma unroll
       for (int i = 0; i < kScaleOps; ++i) {
         const int s = lane + 32 * i, w = s % kScaleWords;
@@ -325,109 +350,102 @@ struct GemvKernel {
 #pragma unroll
       for (int i = 0; i < kZeroOps; ++i)
         zero_first[i] = first_group((lane + 32 * i) / (ZEROS ? kZeroWords : 1) & (16 * MT - 1));
-    };
-    const uint32_t code_dst = ring_at + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));  // h odd: ^ 64
-    auto fetch = [&](uint32_t stage) {
-      if (load.left > 0) {
-        const uint32_t dst = code_dst + stage;
-        if (load_c * kChunk + 32 * (lane & 7) < K) {
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 4; ++h) copy16((h & 1 ? dst ^ 64 : dst) + (i * kTileBytes + h * 512), code_src[i][h]);
+
+      for (int k0 = 0; k0 < K; k0 += kMulPerTeam * kChunk) {
+        if (round && !tc::mbar_wait(bars + 2 * stage + 1, (round - 1) & 1)) {
+          set_dev_error(SP24_ERR_DEVICE_TIMEOUT);
+          copy_wait_all();
+          return;
         }
-        const uint32_t table = ring_at + stage + MT * kTileBytes;
-        if (!near_end) {
+        const uint32_t dst = code_at + stage * (kMulPerTeam * kStage);
+        const uint32_t table = ring_at + stage * (kMulPerTeam * kStage) + MT * kTileBytes + 4 * lane;
+#pragma unroll
+        for (int c = 0; c < kMulPerTeam; ++c) {
+          if (k0 + c * kChunk >= K) break;
+          if (k0 + c * kChunk + 32 * (lane & 7) < K) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                copy16((h & 1 ? dst ^ 64 : dst) + (c * kStage + i * kTileBytes + h * 512), code_src[i][h] + c * (kChunk / 2));
+          }
 #pragma unroll
           for (int i = 0; i < kScaleOps; ++i)
-            if (scale_on[i]) copy4(table + 4 * (lane + 32 * i), scale_src[i]);
-        } else {
+            if (scale_on[i]) {
+              if (near_end)
+                copy4(table + c * kStage + 128 * i, scale_src[i] + c * (2 * kGroups), scales + 2 * groups_total, scales);
+              else
+                copy4(table + c * kStage + 128 * i, scale_src[i] + c * (2 * kGroups));
+            }
 #pragma unroll
-          for (int i = 0; i < kScaleOps; ++i)
-            if (scale_on[i]) copy4(table + 4 * (lane + 32 * i), scale_src[i], scales_end, scales);
+          for (int i = 0; i < kZeroOps; ++i) {
+            const int s = lane + 32 * i, w = s % (ZEROS ? kZeroWords : 1);
+            const int64_t at = zero_first[i] + c * kGroups;
+            if (s < 16 * MT * kZeroWords && 4 * w < ((int)at & 3) + kGroups)
+              copy4(table + c * kStage + kZeroAt + 128 * i, p.zeros + ((at >> 2) * 4 + 4 * w), p.zeros + groups_total,
+                    p.zeros);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < kZeroOps; ++i) {
-          const int s = lane + 32 * i, w = s % (ZEROS ? kZeroWords : 1);
-          const int64_t at = zero_first[i];
-          if (s < 16 * MT * kZeroWords && 4 * w < ((int)at & 3) + kGroups)
-            copy4(table + kZeroAt + 4 * s, p.zeros + ((at >> 2) * 4 + 4 * w), p.zeros + groups_total, p.zeros);
-          zero_first[i] += wk * kGroups;
-        }
+        copy_arrive(bars + 2 * stage);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) code_src[i][h] += wk * (kChunk / 2);
+          for (int h = 0; h < 4; ++h) code_src[i][h] += kMulPerTeam * (kChunk / 2);
 #pragma unroll
-        for (int i = 0; i < kScaleOps; ++i) scale_src[i] += wk * (2 * kGroups);
-        load_c += wk;
-        if (load_c >= chunks) {
-          load.advance(p, col_tiles, teams);
-          load_c = kw;
-          if (load.left > 0) aim();
-        }
+        for (int i = 0; i < kScaleOps; ++i) scale_src[i] += kMulPerTeam * (2 * kGroups);
+#pragma unroll
+        for (int i = 0; i < kZeroOps; ++i) zero_first[i] += kMulPerTeam * kGroups;
+        if (++stage == S) stage = 0, ++round;
       }
-      copy_commit();
-    };
+    }
+    copy_wait_all();
+  }
 
-    if (load.left > 0) aim();
-#pragma unroll
-    for (int s = 0; s < S; ++s) fetch(s * kStage);
+  // ---- a multiplying warp
+  static __device__ __forceinline__ void multiply_all(const GemvW4& p, uint8_t* smem, uint8_t* ring, uint64_t* bars,
+                                                      int warp, int in_cta, int team, int teams) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int kw = warp & (kMulPerTeam - 1);
+    const int64_t cols = columns(p);
+    const int col_tiles = column_tiles(p);
+    const int K = (int)p.K, KG = K / (32 * GB);
+    float* const partials = reinterpret_cast<float*>(smem + kBarriers);  // [buffer][warp][tile][token][row]
+    uint8_t* const x_all = smem + kFixed;
     if (XW) {
       const int pieces = K / 8;
       for (int m = 0; m < (int)p.M; ++m)
-        for (int j = threadIdx.x; j < pieces; j += 32 * kWarps) {
+        for (int j = threadIdx.x; j < pieces; j += 32 * kMulWarps) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)m * pieces + j);
           *reinterpret_cast<uint4*>(x_all + m * x_stride(K) + 16 * j) =
               make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                          __byte_perm(v.y, v.w, 0x7632));
         }
-      __syncthreads();
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + kTeams), "r"(32 * kMulWarps) : "memory");
     }
-    if (use.left <= 0) return;
 
-    // ---- multiplying
-    float tot[MT][NT][4], acc[MT][NT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tot[i][n][k] = 0.0f;
-
+    Walk<kTok> walk;
+    walk.start(p, col_tiles, team, teams);
     // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4); block j + 2 n: ^ 32 n
     const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
-    const uint32_t lm_at = ring_at + lm_row * 128 + 16 * ((lane >> 4) ^ (lane & 7));
+    const uint32_t lm_at = smem_addr(ring) + kw * kStage + lm_row * 128 + 16 * ((lane >> 4) ^ (lane & 7));
+    const uint8_t* const tables = ring + kw * kStage + MT * kTileBytes;
+    float tot[MT][NT][4], acc[MT][NT][4];
+
+    // x of blocks 4 half .. 4 half + 3 of the chunk at entry k, as it stands in memory
     const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
     int group_row[MT];         // (this lane's row of tile i) * KG, as far as its place within a word goes
-    auto aim_use = [&]() {
+    auto read_x = [&](uint4 (&xv)[NT][4], int k, int half, int blocks) {
+      if constexpr (!XW)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int64_t row = use.tok.e * p.N + (SWIGLU ? i * cols : 16 * i) + (int64_t)use.col * kCols + g;
-        group_row[i] = (int)(row & 3) * KG;
-      }
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int m = min(8 * n + g, use.rows() - 1);
-        x_row[n] = XW ? x_all + m * x_stride(K) + 16 * t
-                      : reinterpret_cast<const uint8_t*>(p.x) + ((use.tok.m0 + m) * K + 8 * t) * 2;
-      }
+          for (int j = 0; j < 4; ++j)
+            if (4 * half + j < blocks)
+              xv[n][j] = __ldg(reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * (4 * half + j)));
     };
-    aim_use();
-
-    // x of blocks 4 half .. 4 half + 3 of chunk c, as it stands in memory
-    auto read_x = [&](uint4 (&xv)[NT][4], int c, int half, int blocks) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * half + j < blocks)
-            xv[n][j] = XW ? *reinterpret_cast<const uint4*>(x_row[n] + c * (2 * kChunk) + 64 * (4 * half + j))
-                          : __ldg(reinterpret_cast<const uint4*>(x_row[n] + (int64_t)c * (2 * kChunk) + 64 * (4 * half + j)));
-    };
-    // blocks j, j + 1 of the chunk
-    auto multiply2 = [&](uint32_t stage, int c, int j, const uint4 (&xv)[NT][4], bool both) {
-      const uint8_t* const table = ring + stage + MT * kTileBytes;
+    // blocks j, j + 1 of the chunk in the stage
+    auto multiply2 = [&](uint32_t stage, int k, int j, const uint4 (&xv)[NT][4], bool both) {
+      const uint8_t* const table = tables + stage;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         uint32_t words[4];
@@ -439,10 +457,10 @@ struct GemvKernel {
           uint32_t zl = Expand<XT>::zero(8), zh = zl;
           // rows g and g + 8 start alike within a word
           if (ZEROS) {
-            const int first = group_row[i] + c * kGroups;
+            const int first = group_row[i] + k / (32 * GB);
             const uint8_t* zp = table + kZeroAt + (16 * i + g) * kZeroWords * 4 + (first & 3) + jj / GB;
-            zl = Expand<XT>::zero(zp[0] & 15u);
-            zh = Expand<XT>::zero(zp[8 * kZeroWords * 4] & 15u);
+            zl = Expand<XT>::zero_of(zp[0]);
+            zh = Expand<XT>::zero_of(zp[8 * kZeroWords * 4]);
           }
           uint32_t lo[4], hi[4];
           expand8<XT>(words[2 * jb], zl, lo);
@@ -450,10 +468,14 @@ struct GemvKernel {
           const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            uint4 b = xv[n][jj & 3];
-            if (!XW)
+            uint4 b;
+            if constexpr (XW) {
+              b = *reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * jj);
+            } else {
+              b = xv[n][jj & 3];
               b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
                              __byte_perm(b.y, b.w, 0x7632));
+            }
             if (jj % GB == 0)
               mma16816_first<XT>(acc[i][n], a0, b.x, b.y);
             else
@@ -474,42 +496,57 @@ struct GemvKernel {
         }
       }
     };
-    auto multiply = [&](uint32_t stage, int c, const uint4 (&xv)[NT][4], int half, int blocks) {
+    auto multiply = [&](uint32_t stage, int k, const uint4 (&xv)[NT][4], int half, int blocks) {
 #pragma unroll
       for (int j = 4 * half; j < 4 * half + 4; j += 2)
-        if (j < blocks) multiply2(stage, c, j, xv, j + 1 < blocks);
+        if (j < blocks) multiply2(stage, k, j, xv, j + 1 < blocks);
     };
 
-    uint32_t stage = 0;
-    int c = kw, buffer = 0;
-    while (true) {
-      const int blocks = min(kChunk / 32, K / 32 - kChunk / 32 * c);
-      if (blocks == kChunk / 32) {  // a whole chunk: straight through
-        uint4 x0[NT][4], x1[NT][4];
-        read_x(x0, c, 0, kChunk / 32);
-        copy_wait<S - 1>();
-        __syncwarp();
-        multiply(stage, c, x0, 0, kChunk / 32);
-        read_x(x1, c, 1, kChunk / 32);
-        multiply(stage, c, x1, 1, kChunk / 32);
-      } else {
-        copy_wait<S - 1>();
-        __syncwarp();
-        uint4 x0[NT][4];
-        read_x(x0, c, 0, blocks);
-        multiply(stage, c, x0, 0, blocks);
-        read_x(x0, c, 1, blocks);
-        multiply(stage, c, x0, 1, blocks);
+    int stage = 0, parity = 0, buffer = 0;
+    bool given_up = false;
+    for (; walk.left > 0; walk.advance(p, col_tiles, teams)) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int64_t row = walk.tok.e * p.N + (SWIGLU ? i * cols : 16 * i) + (int64_t)walk.col * kCols + g;
+        group_row[i] = (int)(row & 3) * KG;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tot[i][n][k] = 0.0f;
       }
-      __syncwarp();
-      fetch(stage);
-      stage = stage == (S - 1) * kStage ? 0 : stage + kStage;
-      c += wk;
-      if (c < chunks) continue;
+      const int rows = walk.rows();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int m = min(8 * n + g, rows - 1);
+        x_row[n] = XW ? x_all + m * x_stride(K) + 16 * t
+                      : reinterpret_cast<const uint8_t*>(p.x) + ((walk.tok.m0 + m) * K + 8 * t) * 2;
+      }
+      for (int k = kw * kChunk; k < K + kw * kChunk; k += kMulPerTeam * kChunk) {  // every warp meets every stage
+        const int blocks = min(kChunk / 32, (K - k) / 32);
+        const uint32_t at = stage * (kMulPerTeam * kStage);
+        uint4 x0[NT][4];
+        read_x(x0, k, 0, blocks);
+        if (!given_up && !tc::mbar_wait(bars + 2 * stage, parity)) {
+          set_dev_error(SP24_ERR_DEVICE_TIMEOUT);
+          given_up = true;
+        }
+        __syncwarp();
+        if (blocks == kChunk / 32) {  // a whole chunk: straight through
+          uint4 x1[NT][4];
+          multiply(at, k, x0, 0, kChunk / 32);
+          read_x(x1, k, 1, kChunk / 32);
+          multiply(at, k, x1, 1, kChunk / 32);
+        } else if (blocks > 0) {
+          multiply(at, k, x0, 0, blocks);
+          read_x(x0, k, 1, blocks);
+          multiply(at, k, x0, 1, blocks);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bars + 2 * stage + 1);
+        if (++stage == S) stage = 0, parity ^= 1;
+      }
 
-      // ---- the item is done
-      const int rows = use.rows();
-      float* const mine = partials + (buffer * kWarps + warp) * kPartial;
+      float* const mine = partials + (buffer * kMulWarps + warp) * kPartial;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -518,48 +555,40 @@ struct GemvKernel {
           for (int k = 0; k < 4; ++k) {
             const int m = 8 * n + 2 * t + (k & 1);
             if (m < rows) mine[(i * kTok + m) * 16 + g + 8 * (k >> 1)] = tot[i][n][k] * (1.0f / Expand<XT>::kUnit);
-            tot[i][n][k] = 0.0f;
           }
-      if (wk == 1)
-        __syncwarp();
-      else
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + in_cta), "r"(32 * wk) : "memory");
-      const float* const team_sums = partials + (buffer * kWarps + (in_cta << p.wk_log)) * kPartial;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + in_cta), "r"(32 * kMulPerTeam) : "memory");
+      const float* const sums = partials + (buffer * kMulWarps + in_cta * kMulPerTeam) * kPartial;
       constexpr int kOutTiles = SWIGLU ? 1 : MT;
-      for (int o = kw * 32 + lane; o < rows * kOutTiles * 16; o += 32 * wk) {
+      for (int o = kw * 32 + lane; o < rows * kOutTiles * 16; o += 32 * kMulPerTeam) {
         const int r = o & 15, i = (o >> 4) % kOutTiles, m = (o >> 4) / kOutTiles;
-        const int64_t col = (int64_t)use.col * kCols + 16 * i + r;
+        const int64_t col = (int64_t)walk.col * kCols + 16 * i + r;
         if (col >= cols) continue;
         float v = 0.0f, up = 0.0f;
-        for (int k = 0; k < wk; ++k) {
-          v += team_sums[k * kPartial + (i * kTok + m) * 16 + r];
-          if (SWIGLU) up += team_sums[k * kPartial + (kTok + m) * 16 + r];
+#pragma unroll
+        for (int k = 0; k < kMulPerTeam; ++k) {
+          v += sums[k * kPartial + (i * kTok + m) * 16 + r];
+          if (SWIGLU) up += sums[k * kPartial + (kTok + m) * 16 + r];
         }
         if (SWIGLU) v = v / (1.0f + expf(-v)) * up;
-        const int64_t at = (use.tok.m0 + m) * cols + col;
+        const int64_t out = (walk.tok.m0 + m) * cols + col;
         if (p.y_f32)
-          reinterpret_cast<float*>(p.y)[at] = v;
+          reinterpret_cast<float*>(p.y)[out] = v;
         else
-          reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)W4Half<XT>::put(v);
+          reinterpret_cast<uint16_t*>(p.y)[out] = (uint16_t)W4Half<XT>::put(v);
       }
       buffer ^= 1;
-      c = kw;
-      use.advance(p, col_tiles, teams);
-      if (use.left <= 0) break;
-      aim_use();
     }
-    copy_wait<0>();
   }
 };
 
 template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
-__global__ void __launch_bounds__(32 * kWarps, 1) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
+__global__ void __launch_bounds__(32 * (kMulWarps + kTeams), 1) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
   extern __shared__ __align__(128) uint8_t smem[];
   GemvKernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>::run(p, smem);
 }
 
 template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
-int launch_gemv(GemvW4 p, cudaStream_t s) {
+int launch_gemv(const GemvW4& p, cudaStream_t s) {
   using Kern = GemvKernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>;
   auto kernel = gemv_w4_kernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>;
   static bool raised[64];  // the attribute holds per device
@@ -573,18 +602,11 @@ int launch_gemv(GemvW4 p, cudaStream_t s) {
   const int64_t cols = SWIGLU ? p.N / 2 : p.N, col_tiles = (cols + Kern::kCols - 1) / Kern::kCols;
   // with experts: the sum of ceil(rows / kTok) is at most this
   const int64_t tok_tiles = (p.M + Kern::kTok - 1) / Kern::kTok + (p.offsets ? (p.E < p.M ? p.E : p.M) : 0);
-  const int64_t items = col_tiles * tok_tiles, chunks = (p.K + kChunk - 1) / kChunk;
+  const int64_t items = col_tiles * tok_tiles;
   if (items > INT32_MAX / 2) return SP24_ERR_UNSUPPORTED;
   const int sms = sm_count();
-  // Team size: the fewest rounds of (chunks per warp + about one chunk's time of joining an item).
-  int64_t best = INT64_MAX;
-  for (int k = 0; k <= kWarpsLog && (k == 0 || (1 << k) <= chunks); ++k) {
-    const int64_t teams = (int64_t)sms << (kWarpsLog - k), rounds = (items + teams - 1) / teams;
-    const int64_t cost = rounds * (((chunks + (1 << k) - 1) >> k) * 10 + 7);
-    if (cost < best) best = cost, p.wk_log = k;
-  }
   const int64_t ctas = items < sms ? items : sms;
-  kernel<<<(unsigned)ctas, 32 * kWarps, (size_t)Kern::smem_bytes(p), s>>>(p);
+  kernel<<<(unsigned)ctas, 32 * (kMulWarps + kTeams), (size_t)Kern::smem_bytes(p), s>>>(p);
   return launch_status();
 }
 
@@ -615,7 +637,7 @@ int gemv_by_shape(const GemvW4& p, cudaStream_t s) {
     return by_group<XT, 1, 1, 3, false, true>(p, s);
   if (one && wide && x_bytes <= kSmemMax - GemvKernel<XT, 2, 1, 2, false, true, true, 1>::kFixed)
     return by_group<XT, 2, 1, 2, false, true>(p, s);
-  return wide ? by_group<XT, 2, 2, 2, false, false>(p, s) : by_group<XT, 1, 2, 2, false, false>(p, s);
+  return wide ? by_group<XT, 2, 1, 3, false, false>(p, s) : by_group<XT, 1, 2, 2, false, false>(p, s);
 }
 
 }  // namespace

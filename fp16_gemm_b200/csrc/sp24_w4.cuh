@@ -27,10 +27,12 @@ struct GemvW4 {
   const int32_t* offsets;  // grouped: E + 1
   void* y;
   int64_t M, E, N, K;
-  int scale_dtype, group, act, y_f32;
+  int scale_dtype, group, y_f32;
 };
 
 int gemv_w4_bf16(const GemvW4& p, cudaStream_t s);
 int gemv_w4_f16(const GemvW4& p, cudaStream_t s);
+int gemv_w4_swiglu_bf16(const GemvW4& p, cudaStream_t s);
+int gemv_w4_swiglu_f16(const GemvW4& p, cudaStream_t s);
 
 }  // namespace sp24

@@ -242,9 +242,10 @@ struct Walk {
 //
 // Persistent, one CTA per SM of four teams, each of which walks work items of its own: one warp
 // copies (cp.async, S stages of four chunks of 256 entries ahead, across the items' borders), four
-// multiply, each a chunk of every four along K; mbarriers tell the stages full and empty.  The
-// partial sums of the four meet in shared memory in a fixed order, in two buffers that take turns, so
-// one barrier of the team per item is enough.
+// multiply, each a chunk of every four; mbarriers tell the stages full and empty.  The four chunks
+// follow each other along K (WK 4), or, where K has no more than two, pairs of them along the columns
+// (WK 2).  The partial sums of the warps that share K meet in shared memory in a fixed order, in two buffers
+// that take turns, so one barrier of the team per item is enough.
 //
 // An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of a 32-entry block
 // of rows g and g + 8; the MMA may sum K in any order, so the pairs that expand8 gives are fed as
@@ -255,22 +256,29 @@ struct Walk {
 //
 // Waits are bounded by the library's wait limit: a warp that gives up records it, does not wait again
 // and passes through the rest of its items, so every barrier is still met.
-template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
+template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW, bool ZEROS, int GB>
 struct GemvKernel {
   static constexpr int kTok = 8 * NT;
-  static constexpr int kCols = SWIGLU ? 16 : 16 * MT;    // output columns of an item
-  static constexpr int kGroups = kChunk / 32 / GB;       // groups per chunk
-  // A chunk's scales of one row are 2 kGroups bytes at any even place, its zero points kGroups bytes
-  // at any place: the aligned words that they may touch are copied.  A chunk has an even number of
-  // groups, so a row's scales keep their place within a word from chunk to chunk.
-  static constexpr int kScaleWords = kGroups / 2 + 1;
-  static constexpr int kZeroWords = ZEROS ? (kGroups + 2) / 4 + 1 : 0;
-  static constexpr int kZeroAt = 16 * MT * kScaleWords * 4;                     // in bytes, behind the scales
-  static constexpr int kStage = MT * kTileBytes + (kZeroAt + 16 * MT * kZeroWords * 4 + 127) / 128 * 128;
+  static constexpr int kCols = SWIGLU ? 16 : 16 * MT;       // output columns of a warp's tiles
+  static constexpr int kSubs = kMulPerTeam / WK;            // of them beside each other in an item
+  static constexpr int kItemCols = kCols * kSubs;
+  static constexpr int kStep = kChunk * WK;                 // entries of K per stage
+  static constexpr int kGroups = kChunk / 32 / GB;          // groups per chunk
+  static constexpr int kStepGroups = kGroups * WK;          // and per stage: at least four
+  // A stage: four chunks of codes, then the scales and the zero points of its rows.  A row's scales are
+  // 2 kStepGroups bytes at any even place, its zero points kStepGroups bytes at any place: where rows
+  // are 16-byte aligned they are copied as such, otherwise the aligned words that they may touch.
+  // The rows of either table are an odd number of 16-byte pieces apart: eight rows meet no bank twice.
+  static constexpr int kRows = 16 * MT * kSubs;
+  static constexpr int odd_pieces(int bytes) { return ((bytes + 15) / 16 | 1) * 16; }
+  static constexpr int kScaleWords = kStepGroups / 2 + 1, kScaleRow = odd_pieces(4 * kScaleWords);
+  static constexpr int kZeroWords = (kStepGroups + 2) / 4 + 1, kZeroRow = ZEROS ? odd_pieces(4 * kZeroWords) : 0;
+  static constexpr int kScaleAt = kMulPerTeam * MT * kTileBytes, kZeroAt = kScaleAt + kRows * kScaleRow;
+  static constexpr int kStage = (kZeroAt + kRows * kZeroRow + 127) / 128 * 128;
   static constexpr int kPartial = MT * kTok * 16;                               // floats per warp and buffer
   static constexpr int kBarriers = 1024;                                        // bytes
   static constexpr int kRing = kBarriers + 2 * kMulWarps * kPartial * 4;
-  static constexpr int kFixed = kRing + kMulWarps * S * kStage;
+  static constexpr int kFixed = kRing + kTeams * S * kStage;
 
   static __host__ __device__ __forceinline__ int x_stride(int K) {
     return (2 * K + 127) / 128 * 128 + 64;  // two neighbouring rows of x never meet in a bank
@@ -292,7 +300,7 @@ struct GemvKernel {
     const bool copies = warp >= kMulWarps;
     const int in_cta = copies ? warp - kMulWarps : warp / kMulPerTeam;
     const int team = in_cta * gridDim.x + blockIdx.x, teams = gridDim.x * kTeams;
-    uint8_t* const ring = smem + kRing + in_cta * (kMulPerTeam * S * kStage);  // [stage][chunk of the four]
+    uint8_t* const ring = smem + kRing + in_cta * (S * kStage);
     if (copies)
       copy(p, ring, bars + 2 * S * in_cta, team, teams);
     else
@@ -301,7 +309,7 @@ struct GemvKernel {
 
   static __device__ __forceinline__ int64_t columns(const GemvW4& p) { return SWIGLU ? p.N / 2 : p.N; }
   static __device__ __forceinline__ int column_tiles(const GemvW4& p) {
-    return (int)((columns(p) + kCols - 1) / kCols);
+    return (int)((columns(p) + kItemCols - 1) / kItemCols);
   }
 
   // ---- the copying warp: lane l copies piece l & 7 of rows (l >> 3) + 4 h of each of the four chunks
@@ -313,88 +321,115 @@ struct GemvKernel {
     const int64_t groups_total = p.E * p.N * KG;
     const uint8_t* const scales = reinterpret_cast<const uint8_t*>(p.scales);
     const uint32_t ring_at = smem_addr(ring);
+    const bool scale_pieces = kStepGroups % 8 == 0 && KG % 8 == 0 && reinterpret_cast<uintptr_t>(scales) % 16 == 0;
+    const bool zero_pieces = kStepGroups % 16 == 0 && KG % 16 == 0 && reinterpret_cast<uintptr_t>(p.zeros) % 16 == 0;
     // a row's pieces change places by its number: row r's piece i stands at i ^ (r & 7)
     const uint32_t code_at = ring_at + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));  // h odd: ^ 64
-    constexpr int kScaleOps = (16 * MT * kScaleWords + 31) / 32, kZeroOps = (16 * MT * kZeroWords + 31) / 32;
     Walk<kTok> walk;
     walk.start(p, col_tiles, team, teams);
     int stage = 0, round = 0;
     for (; walk.left > 0; walk.advance(p, col_tiles, teams)) {
-      const int left = (int)min((int64_t)kCols, cols - (int64_t)walk.col * kCols);  // columns of this item
-      const int64_t row0 = walk.tok.e * p.N + (int64_t)walk.col * kCols;
-      // a copied word may reach past the arrays' ends: a row's last chunk may name up to seven groups
-      // too many, of as many further rows
-      const bool near_end = row0 + (SWIGLU ? cols : 0) + kCols + 8 >= p.E * p.N;
-      // rows past the end repeat the last one; they are computed and not stored
+      const int left = (int)min((int64_t)kItemCols, cols - (int64_t)walk.col * kItemCols);  // columns of this item
+      const int64_t row0 = walk.tok.e * p.N + (int64_t)walk.col * kItemCols;
+      // a copied word may reach past the arrays' ends: a stage may name groups past a row's last
+      const bool near_end = row0 + (SWIGLU ? cols : 0) + kItemCols + kStepGroups >= p.E * p.N;
       const uint8_t* code_src[MT][4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const uint8_t* const src = p.codes + (row0 + (SWIGLU ? i * cols : 0)) * (K / 2) + 16 * (lane & 7);
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int h = 0; h < 4; ++h)
-          code_src[i][h] = src + (uint32_t)(min((SWIGLU ? 0 : 16 * i) + (lane >> 3) + 4 * h, left - 1) * (K / 2));
-      }
-      auto first_group = [&](int r) {
-        return (row0 + (SWIGLU ? (r >> 4) * cols : 0)) * KG + min(SWIGLU ? r & 15 : r, left - 1) * KG;
-      };
-      const uint8_t* scale_src[kScaleOps];
-      bool scale_on[kScaleOps];
-      int64_t zero_first[kZeroOps ? kZeroOps : 1];
-#pragma unroll
-      for (int i = 0; i < kScaleOps; ++i) {
-        const int s = lane + 32 * i, w = s % kScaleWords;
-        const int64_t at = first_group(s / kScaleWords & (16 * MT - 1));
-        scale_on[i] = s < 16 * MT * kScaleWords && 2 * w < ((int)at & 1) + kGroups;
-        scale_src[i] = scales + (at >> 1) * 4 + 4 * w;
-      }
-#pragma unroll
-      for (int i = 0; i < kZeroOps; ++i)
-        zero_first[i] = first_group((lane + 32 * i) / (ZEROS ? kZeroWords : 1) & (16 * MT - 1));
+          code_src[i][h] = p.codes + (row0 + (SWIGLU ? i * cols : 16 * i) + (lane >> 3) + 4 * h) * (K / 2) + 16 * (lane & 7);
+      // the first group of table row r's weight row: of the item's first row, and from there on
+      const int64_t base0 = row0 * KG, base1 = SWIGLU ? (row0 + cols) * KG : base0;
+      auto base = [&](int r) { return SWIGLU && (r & 16) ? base1 : base0; };
+      auto row_of = [&](int r) { return SWIGLU ? (r & 15) + (r >> 5) * 16 : r; };  // within the item
 
-      for (int k0 = 0; k0 < K; k0 += kMulPerTeam * kChunk) {
+      for (int k0 = 0; k0 < K; k0 += kStep) {
         if (round && !tc::mbar_wait(bars + 2 * stage + 1, (round - 1) & 1)) {
           set_dev_error(SP24_ERR_DEVICE_TIMEOUT);
           copy_wait_all();
           return;
         }
-        const uint32_t dst = code_at + stage * (kMulPerTeam * kStage);
-        const uint32_t table = ring_at + stage * (kMulPerTeam * kStage) + MT * kTileBytes + 4 * lane;
+        const uint32_t dst = code_at + stage * kStage;
+        if (left == kItemCols && k0 + kStep <= K) {
 #pragma unroll
-        for (int c = 0; c < kMulPerTeam; ++c) {
-          if (k0 + c * kChunk >= K) break;
-          if (k0 + c * kChunk + 32 * (lane & 7) < K) {
+          for (int c = 0; c < kMulPerTeam; ++c) {
+            const int64_t on = c % WK * (kChunk / 2) + (c < WK ? 0 : (int64_t)(c / WK * kCols) * (K / 2));
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
               for (int h = 0; h < 4; ++h)
-                copy16((h & 1 ? dst ^ 64 : dst) + (c * kStage + i * kTileBytes + h * 512), code_src[i][h] + c * (kChunk / 2));
+                copy16((h & 1 ? dst ^ 64 : dst) + ((c * MT + i) * kTileBytes + h * 512), code_src[i][h] + on);
           }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kMulPerTeam; ++c) {
+            const int col = c / WK * kCols;
+            const int64_t on = c % WK * (kChunk / 2) + (int64_t)col * (K / 2);
+            if (k0 + c % WK * kChunk + 32 * (lane & 7) < K)
 #pragma unroll
-          for (int i = 0; i < kScaleOps; ++i)
-            if (scale_on[i]) {
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                  if (col + (SWIGLU ? 0 : 16 * i) + (lane >> 3) + 4 * h < left)
+                    copy16((h & 1 ? dst ^ 64 : dst) + ((c * MT + i) * kTileBytes + h * 512), code_src[i][h] + on);
+          }
+        }
+        const int g0 = k0 / (32 * GB);
+        const uint32_t scale_at = ring_at + stage * kStage + kScaleAt, zero_at = ring_at + stage * kStage + kZeroAt;
+        if (scale_pieces) {
+          constexpr int kPieces = kStepGroups / 8 ? kStepGroups / 8 : 1;
+#pragma unroll
+          for (int s0 = 0; s0 < kRows * kPieces; s0 += 32) {
+            const int s = s0 + lane, r = s / kPieces, q = s % kPieces;
+            if (s < kRows * kPieces && row_of(r) < left && g0 + 8 * q < KG)
+              copy16(scale_at + r * kScaleRow + 16 * q, scales + 2 * base(r) + 2 * (row_of(r) * KG + g0 + 8 * q));
+          }
+        } else {
+#pragma unroll
+          for (int s0 = 0; s0 < kRows * kScaleWords; s0 += 32) {
+            const int s = s0 + lane, r = s / kScaleWords, w = s % kScaleWords;
+            const int64_t b = base(r);
+            const int at = ((int)b & 1) + row_of(r) * KG + g0;  // from the aligned word that b is in
+            if (s < kRows * kScaleWords && row_of(r) < left && 2 * w < (at & 1) + kStepGroups) {
+              const uint8_t* const src = scales + (b >> 1) * 4 + ((at >> 1) + w) * 4;
               if (near_end)
-                copy4(table + c * kStage + 128 * i, scale_src[i] + c * (2 * kGroups), scales + 2 * groups_total, scales);
+                copy4(scale_at + r * kScaleRow + 4 * w, src, scales + 2 * groups_total, scales);
               else
-                copy4(table + c * kStage + 128 * i, scale_src[i] + c * (2 * kGroups));
+                copy4(scale_at + r * kScaleRow + 4 * w, src);
             }
+          }
+        }
+        if constexpr (ZEROS) {
+          if (zero_pieces) {
+            constexpr int kPieces = kStepGroups / 16 ? kStepGroups / 16 : 1;
 #pragma unroll
-          for (int i = 0; i < kZeroOps; ++i) {
-            const int s = lane + 32 * i, w = s % (ZEROS ? kZeroWords : 1);
-            const int64_t at = zero_first[i] + c * kGroups;
-            if (s < 16 * MT * kZeroWords && 4 * w < ((int)at & 3) + kGroups)
-              copy4(table + c * kStage + kZeroAt + 128 * i, p.zeros + ((at >> 2) * 4 + 4 * w), p.zeros + groups_total,
-                    p.zeros);
+            for (int s0 = 0; s0 < kRows * kPieces; s0 += 32) {
+              const int s = s0 + lane, r = s / kPieces, q = s % kPieces;
+              if (s < kRows * kPieces && row_of(r) < left && g0 + 16 * q < KG)
+                copy16(zero_at + r * kZeroRow + 16 * q, p.zeros + base(r) + (row_of(r) * KG + g0 + 16 * q));
+            }
+          } else {
+#pragma unroll
+            for (int s0 = 0; s0 < kRows * kZeroWords; s0 += 32) {
+              const int s = s0 + lane, r = s / kZeroWords, w = s % kZeroWords;
+              const int64_t b = base(r);
+              const int at = ((int)b & 3) + row_of(r) * KG + g0;
+              if (s < kRows * kZeroWords && row_of(r) < left && 4 * w < (at & 3) + kStepGroups) {
+                const uint8_t* const src = p.zeros + (b >> 2) * 4 + ((at >> 2) + w) * 4;
+                if (near_end)
+                  copy4(zero_at + r * kZeroRow + 4 * w, src, p.zeros + groups_total, p.zeros);
+                else
+                  copy4(zero_at + r * kZeroRow + 4 * w, src);
+              }
+            }
           }
         }
         copy_arrive(bars + 2 * stage);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) code_src[i][h] += kMulPerTeam * (kChunk / 2);
-#pragma unroll
-        for (int i = 0; i < kScaleOps; ++i) scale_src[i] += kMulPerTeam * (2 * kGroups);
-#pragma unroll
-        for (int i = 0; i < kZeroOps; ++i) zero_first[i] += kMulPerTeam * kGroups;
+          for (int h = 0; h < 4; ++h) code_src[i][h] += kStep / 2;
         if (++stage == S) stage = 0, ++round;
       }
     }
@@ -405,7 +440,7 @@ struct GemvKernel {
   static __device__ __forceinline__ void multiply_all(const GemvW4& p, uint8_t* smem, uint8_t* ring, uint64_t* bars,
                                                       int warp, int in_cta, int team, int teams) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int kw = warp & (kMulPerTeam - 1);
+    const int in_team = warp & (kMulPerTeam - 1), kw = in_team % WK, sub = in_team / WK;
     const int64_t cols = columns(p);
     const int col_tiles = column_tiles(p);
     const int K = (int)p.K, KG = K / (32 * GB);
@@ -427,25 +462,26 @@ struct GemvKernel {
     walk.start(p, col_tiles, team, teams);
     // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4); block j + 2 n: ^ 32 n
     const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
-    const uint32_t lm_at = smem_addr(ring) + kw * kStage + lm_row * 128 + 16 * ((lane >> 4) ^ (lane & 7));
-    const uint8_t* const tables = ring + kw * kStage + MT * kTileBytes;
+    const uint32_t lm_at = smem_addr(ring) + in_team * (MT * kTileBytes) + lm_row * 128 + 16 * ((lane >> 4) ^ (lane & 7));
+    const uint8_t* const scale_row = ring + kScaleAt + (sub * 16 * MT + g) * kScaleRow + 2 * kw * kGroups;
+    const uint8_t* const zero_row = ring + kZeroAt + (sub * 16 * MT + g) * kZeroRow + kw * kGroups;
     float tot[MT][NT][4], acc[MT][NT][4];
 
-    // x of blocks 4 half .. 4 half + 3 of the chunk at entry k, as it stands in memory
+    // x of kAhead blocks of the chunk at entry k, as it stands in memory, read one such part ahead
+    constexpr int kAhead = NT == 1 ? 4 : 2, kParts = kChunk / 32 / kAhead;
     const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
-    int group_row[MT];         // (this lane's row of tile i) * KG, as far as its place within a word goes
-    auto read_x = [&](uint4 (&xv)[NT][4], int k, int half, int blocks) {
+    int scale_odd[MT], zero_odd[MT];  // where the first group of its row of tile i stands within a word
+    auto read_x = [&](uint4 (&xv)[NT][kAhead], int k, int part, int blocks) {
       if constexpr (!XW)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (4 * half + j < blocks)
-              xv[n][j] = __ldg(reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * (4 * half + j)));
+          for (int j = 0; j < kAhead; ++j)
+            if (kAhead * part + j < blocks)
+              xv[n][j] = __ldg(reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * (kAhead * part + j)));
     };
     // blocks j, j + 1 of the chunk in the stage
-    auto multiply2 = [&](uint32_t stage, int k, int j, const uint4 (&xv)[NT][4], bool both) {
-      const uint8_t* const table = tables + stage;
+    auto multiply2 = [&](uint32_t stage, int k, int j, const uint4 (&xv)[NT][kAhead], bool both) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         uint32_t words[4];
@@ -457,10 +493,9 @@ struct GemvKernel {
           uint32_t zl = Expand<XT>::zero(8), zh = zl;
           // rows g and g + 8 start alike within a word
           if (ZEROS) {
-            const int first = group_row[i] + k / (32 * GB);
-            const uint8_t* zp = table + kZeroAt + (16 * i + g) * kZeroWords * 4 + (first & 3) + jj / GB;
+            const uint8_t* zp = zero_row + stage + zero_odd[i] + 16 * i * kZeroRow + jj / GB;
             zl = Expand<XT>::zero_of(zp[0]);
-            zh = Expand<XT>::zero_of(zp[8 * kZeroWords * 4]);
+            zh = Expand<XT>::zero_of(zp[8 * kZeroRow]);
           }
           uint32_t lo[4], hi[4];
           expand8<XT>(words[2 * jb], zl, lo);
@@ -472,7 +507,7 @@ struct GemvKernel {
             if constexpr (XW) {
               b = *reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * jj);
             } else {
-              b = xv[n][jj & 3];
+              b = xv[n][jj % kAhead];
               b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
                              __byte_perm(b.y, b.w, 0x7632));
             }
@@ -483,9 +518,9 @@ struct GemvKernel {
             mma16816<XT>(acc[i][n], a1, b.z, b.w);
           }
           if ((jj + 1) % GB == 0) {
-            const uint8_t* sp = table + (16 * i + g) * kScaleWords * 4 + 2 * ((group_row[i] & 1) + jj / GB);
+            const uint8_t* sp = scale_row + stage + scale_odd[i] + 16 * i * kScaleRow + 2 * (jj / GB);
             const uint32_t l = *reinterpret_cast<const uint16_t*>(sp);
-            const uint32_t h = *reinterpret_cast<const uint16_t*>(sp + 8 * kScaleWords * 4);
+            const uint32_t h = *reinterpret_cast<const uint16_t*>(sp + 8 * kScaleRow);
             const float sl = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(l) : W4Half<SP24_F16>::get(l);
             const float sh = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(h) : W4Half<SP24_F16>::get(h);
 #pragma unroll
@@ -496,9 +531,9 @@ struct GemvKernel {
         }
       }
     };
-    auto multiply = [&](uint32_t stage, int k, const uint4 (&xv)[NT][4], int half, int blocks) {
+    auto multiply = [&](uint32_t stage, int k, const uint4 (&xv)[NT][kAhead], int part, int blocks) {
 #pragma unroll
-      for (int j = 4 * half; j < 4 * half + 4; j += 2)
+      for (int j = kAhead * part; j < kAhead * (part + 1); j += 2)
         if (j < blocks) multiply2(stage, k, j, xv, j + 1 < blocks);
     };
 
@@ -507,8 +542,10 @@ struct GemvKernel {
     for (; walk.left > 0; walk.advance(p, col_tiles, teams)) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int64_t row = walk.tok.e * p.N + (SWIGLU ? i * cols : 16 * i) + (int64_t)walk.col * kCols + g;
-        group_row[i] = (int)(row & 3) * KG;
+        // further tiles of 16 rows: the same place
+        const int64_t row = walk.tok.e * p.N + (SWIGLU ? i * cols : 0) + (int64_t)walk.col * kItemCols + g;
+        scale_odd[i] = (int)(row & 1) * (KG & 1) * 2;
+        zero_odd[i] = (int)(row & 3) * KG & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -521,25 +558,28 @@ struct GemvKernel {
         x_row[n] = XW ? x_all + m * x_stride(K) + 16 * t
                       : reinterpret_cast<const uint8_t*>(p.x) + ((walk.tok.m0 + m) * K + 8 * t) * 2;
       }
-      for (int k = kw * kChunk; k < K + kw * kChunk; k += kMulPerTeam * kChunk) {  // every warp meets every stage
+      for (int k = kw * kChunk; k < K + kw * kChunk; k += kStep) {  // every warp meets every stage
         const int blocks = min(kChunk / 32, (K - k) / 32);
-        const uint32_t at = stage * (kMulPerTeam * kStage);
-        uint4 x0[NT][4];
-        read_x(x0, k, 0, blocks);
+        const uint32_t at = stage * kStage;
+        uint4 x[2][NT][kAhead];
+        read_x(x[0], k, 0, blocks);
         if (!given_up && !tc::mbar_wait(bars + 2 * stage, parity)) {
           set_dev_error(SP24_ERR_DEVICE_TIMEOUT);
           given_up = true;
         }
         __syncwarp();
         if (blocks == kChunk / 32) {  // a whole chunk: straight through
-          uint4 x1[NT][4];
-          multiply(at, k, x0, 0, kChunk / 32);
-          read_x(x1, k, 1, kChunk / 32);
-          multiply(at, k, x1, 1, kChunk / 32);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            if (part + 1 < kParts) read_x(x[(part + 1) & 1], k, part + 1, kChunk / 32);
+            multiply(at, k, x[part & 1], part, kChunk / 32);
+          }
         } else if (blocks > 0) {
-          multiply(at, k, x0, 0, blocks);
-          read_x(x0, k, 1, blocks);
-          multiply(at, k, x0, 1, blocks);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            multiply(at, k, x[0], part, blocks);
+            if (part + 1 < kParts) read_x(x[0], k, part + 1, blocks);
+          }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bars + 2 * stage + 1);
@@ -559,13 +599,15 @@ struct GemvKernel {
       asm volatile("bar.sync %0, %1;" ::"r"(1 + in_cta), "r"(32 * kMulPerTeam) : "memory");
       const float* const sums = partials + (buffer * kMulWarps + in_cta * kMulPerTeam) * kPartial;
       constexpr int kOutTiles = SWIGLU ? 1 : MT;
-      for (int o = kw * 32 + lane; o < rows * kOutTiles * 16; o += 32 * kMulPerTeam) {
-        const int r = o & 15, i = (o >> 4) % kOutTiles, m = (o >> 4) / kOutTiles;
-        const int64_t col = (int64_t)walk.col * kCols + 16 * i + r;
+      constexpr int kTiles = kItemCols / 16;
+      for (int o = in_team * 32 + lane; o < rows * kTiles * 16; o += 32 * kMulPerTeam) {
+        const int r = o & 15, tile = (o >> 4) % kTiles, m = (o >> 4) / kTiles;
+        const int64_t col = (int64_t)walk.col * kItemCols + 16 * tile + r;
         if (col >= cols) continue;
+        const int i = tile % kOutTiles, first = tile / kOutTiles * WK;
         float v = 0.0f, up = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kMulPerTeam; ++k) {
+        for (int k = first; k < first + WK; ++k) {
           v += sums[k * kPartial + (i * kTok + m) * 16 + r];
           if (SWIGLU) up += sums[k * kPartial + (kTok + m) * 16 + r];
         }
@@ -581,16 +623,16 @@ struct GemvKernel {
   }
 };
 
-template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
+template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW, bool ZEROS, int GB>
 __global__ void __launch_bounds__(32 * (kMulWarps + kTeams), 1) gemv_w4_kernel(const __grid_constant__ GemvW4 p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  GemvKernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>::run(p, smem);
+  GemvKernel<XT, NT, MT, S, WK, SWIGLU, XW, ZEROS, GB>::run(p, smem);
 }
 
-template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW, bool ZEROS, int GB>
+template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW, bool ZEROS, int GB>
 int launch_gemv(const GemvW4& p, cudaStream_t s) {
-  using Kern = GemvKernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>;
-  auto kernel = gemv_w4_kernel<XT, NT, MT, S, SWIGLU, XW, ZEROS, GB>;
+  using Kern = GemvKernel<XT, NT, MT, S, WK, SWIGLU, XW, ZEROS, GB>;
+  auto kernel = gemv_w4_kernel<XT, NT, MT, S, WK, SWIGLU, XW, ZEROS, GB>;
   static bool raised[64];  // the attribute holds per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SP24_ERR_CUDA;
@@ -599,7 +641,7 @@ int launch_gemv(const GemvW4& p, cudaStream_t s) {
       return SP24_ERR_CUDA;
     raised[dev] = true;
   }
-  const int64_t cols = SWIGLU ? p.N / 2 : p.N, col_tiles = (cols + Kern::kCols - 1) / Kern::kCols;
+  const int64_t cols = SWIGLU ? p.N / 2 : p.N, col_tiles = (cols + Kern::kItemCols - 1) / Kern::kItemCols;
   // with experts: the sum of ceil(rows / kTok) is at most this
   const int64_t tok_tiles = (p.M + Kern::kTok - 1) / Kern::kTok + (p.offsets ? (p.E < p.M ? p.E : p.M) : 0);
   const int64_t items = col_tiles * tok_tiles;
@@ -610,34 +652,44 @@ int launch_gemv(const GemvW4& p, cudaStream_t s) {
   return launch_status();
 }
 
-template <int XT, int NT, int MT, int S, bool SWIGLU, bool XW>
+template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW>
 int by_group(const GemvW4& p, cudaStream_t s) {
   if (p.zeros) {
-    if (p.group == 128) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, true, 4>(p, s);
-    if (p.group == 64) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, true, 2>(p, s);
-    return launch_gemv<XT, NT, MT, S, SWIGLU, XW, true, 1>(p, s);
+    if (p.group == 128) return launch_gemv<XT, NT, MT, S, WK, SWIGLU, XW, true, 4>(p, s);
+    if (p.group == 64) return launch_gemv<XT, NT, MT, S, WK, SWIGLU, XW, true, 2>(p, s);
+    return launch_gemv<XT, NT, MT, S, WK, SWIGLU, XW, true, 1>(p, s);
   }
-  if (p.group == 128) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, false, 4>(p, s);
-  if (p.group == 64) return launch_gemv<XT, NT, MT, S, SWIGLU, XW, false, 2>(p, s);
-  return launch_gemv<XT, NT, MT, S, SWIGLU, XW, false, 1>(p, s);
+  if (p.group == 128) return launch_gemv<XT, NT, MT, S, WK, SWIGLU, XW, false, 4>(p, s);
+  if (p.group == 64) return launch_gemv<XT, NT, MT, S, WK, SWIGLU, XW, false, 2>(p, s);
+  return launch_gemv<XT, NT, MT, S, WK, SWIGLU, XW, false, 1>(p, s);
+}
+
+// x as a whole in shared memory where it fits beside the ring, and is one tile's rows of one matrix.
+template <int XT, int NT, int MT, int S, int WK, bool SWIGLU>
+bool x_fits(const GemvW4& p) {
+  using Kern = GemvKernel<XT, NT, MT, S, WK, SWIGLU, true, true, 1>;  // the largest stages
+  return !p.offsets && p.M <= Kern::kTok && p.M * (int64_t)Kern::x_stride((int)p.K) <= kSmemMax - Kern::kFixed;
 }
 
 template <int XT>
-int gemv_by_shape(const GemvW4& p, cudaStream_t s) {
+int gemv_w4_plain(const GemvW4& p, cudaStream_t s) {
+  if (p.K <= 2 * kChunk)
+    return x_fits<XT, 1, 1, 3, 2, false>(p) ? by_group<XT, 1, 1, 3, 2, false, true>(p, s)
+                                            : by_group<XT, 1, 2, 2, 2, false, false>(p, s);
+  if (x_fits<XT, 1, 1, 3, 4, false>(p)) return by_group<XT, 1, 1, 3, 4, false, true>(p, s);
   // sixteen rows of x per tile only where eight would leave a second tile per matrix
-  const bool wide = p.M > 8 * p.E;
-  const int64_t x_bytes = p.M * ((2 * p.K + 127) / 128 * 128 + 64);
-  const bool one = !p.offsets && p.M <= 16;  // one tile of x for the whole matrix
-  if (p.act == SP24_ACT_SWIGLU) {
-    if (one && !wide && x_bytes <= kSmemMax - GemvKernel<XT, 1, 2, 2, true, true, true, 1>::kFixed)
-      return by_group<XT, 1, 2, 2, true, true>(p, s);
-    return wide ? by_group<XT, 2, 2, 2, true, false>(p, s) : by_group<XT, 1, 2, 2, true, false>(p, s);
-  }
-  if (one && !wide && x_bytes <= kSmemMax - GemvKernel<XT, 1, 1, 3, false, true, true, 1>::kFixed)
-    return by_group<XT, 1, 1, 3, false, true>(p, s);
-  if (one && wide && x_bytes <= kSmemMax - GemvKernel<XT, 2, 1, 2, false, true, true, 1>::kFixed)
-    return by_group<XT, 2, 1, 2, false, true>(p, s);
-  return wide ? by_group<XT, 2, 1, 3, false, false>(p, s) : by_group<XT, 1, 2, 2, false, false>(p, s);
+  if (p.M <= 8 * p.E) return by_group<XT, 1, 2, 2, 4, false, false>(p, s);
+  return x_fits<XT, 2, 1, 2, 4, false>(p) ? by_group<XT, 2, 1, 2, 4, false, true>(p, s)
+                                          : by_group<XT, 2, 1, 3, 4, false, false>(p, s);
+}
+
+template <int XT>
+int gemv_w4_swiglu(const GemvW4& p, cudaStream_t s) {
+  if (p.K <= 2 * kChunk)
+    return x_fits<XT, 1, 2, 2, 2, true>(p) ? by_group<XT, 1, 2, 2, 2, true, true>(p, s)
+                                           : by_group<XT, 1, 2, 2, 2, true, false>(p, s);
+  return x_fits<XT, 1, 2, 2, 4, true>(p) ? by_group<XT, 1, 2, 2, 4, true, true>(p, s)
+                                         : by_group<XT, 1, 2, 2, 4, true, false>(p, s);
 }
 
 }  // namespace

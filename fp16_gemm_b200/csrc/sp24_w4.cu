@@ -204,7 +204,7 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   if (!aligned(y, yb) || !aligned(offsets, 4)) return SP24_ERR_ALIGN;
   if (K == 0) return cudaMemsetAsync(y, 0, (size_t)(M * cols * yb), s) == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
   if (!x || !w->codes || !w->scales) return SP24_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 4) || !aligned(w->zeros, 4)) return SP24_ERR_ALIGN;
+  if (!aligned(x, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 16) || !aligned(w->zeros, 16)) return SP24_ERR_ALIGN;
   const GemvW4 p{x, w->codes, reinterpret_cast<const uint16_t*>(w->scales), w->zeros, grouped ? offsets : nullptr, y,
                  M, E, N, K, w->scale_dtype, w->group, y_dtype == SP24_F32};
   if (act == SP24_ACT_SWIGLU) return x_dtype == SP24_BF16 ? gemv_w4_swiglu_bf16(p, s) : gemv_w4_swiglu_f16(p, s);
@@ -265,7 +265,7 @@ extern "C" int sp24_quantize_w4(const void* w, int dtype, int64_t rows, int64_t 
   if (!zeros != !with_zeros) return SP24_ERR_INVALID_ARG;
   if (rows == 0 || K == 0) return SP24_OK;
   if (!w || !codes || !scales) return SP24_ERR_INVALID_ARG;
-  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(zeros, 4)) return SP24_ERR_ALIGN;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(zeros, 16)) return SP24_ERR_ALIGN;
   return dtype == SP24_BF16
              ? quantize_by_group<SP24_BF16>(group, w, rows * K, with_zeros, codes, scales, zeros, as_stream(stream))
              : quantize_by_group<SP24_F16>(group, w, rows * K, with_zeros, codes, scales, zeros, as_stream(stream));
@@ -279,7 +279,7 @@ extern "C" int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_
   if (st) return st;
   if (rows == 0 || K == 0) return SP24_OK;
   if (!w->codes || !w->scales || !out) return SP24_ERR_INVALID_ARG;
-  if (!aligned(w->codes, 16) || !aligned(w->scales, 4) || !aligned(w->zeros, 4) || !aligned(out, 16)) return SP24_ERR_ALIGN;
+  if (!aligned(w->codes, 16) || !aligned(w->scales, 16) || !aligned(w->zeros, 16) || !aligned(out, 16)) return SP24_ERR_ALIGN;
   const int64_t vecs = rows * (K / 8);
   if (out_dtype == SP24_F32) return dequantize<SP24_F32>(w, vecs, out, as_stream(stream));
   if (out_dtype == SP24_BF16) return dequantize<SP24_BF16>(w, vecs, out, as_stream(stream));

@@ -17,13 +17,10 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src));
-}
-// The part of the four bytes that lies before `end`, zeros for the rest; `base` is the array's start.
-__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src, const uint8_t* end, const uint8_t* base) {
-  const int n = src + 4 <= end ? 4 : src < end ? (int)(end - src) : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(n ? src : base), "r"(n));
+// The part of the sixteen bytes that lies before `end`, zeros for the rest; `base` is the array's start.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, const uint8_t* end, const uint8_t* base) {
+  const int n = src + 16 <= end ? 16 : src < end ? (int)(end - src) : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(n ? src : base), "r"(n));
 }
 // The barrier gets this thread's arrival when all its copies so far have landed.
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
@@ -266,13 +263,12 @@ struct GemvKernel {
   static constexpr int kGroups = kChunk / 32 / GB;          // groups per chunk
   static constexpr int kStepGroups = kGroups * WK;          // and per stage: at least four
   // A stage: four chunks of codes, then the scales and the zero points of its rows.  A row's scales are
-  // 2 kStepGroups bytes at any even place, its zero points kStepGroups bytes at any place: where rows
-  // are 16-byte aligned they are copied as such, otherwise the aligned words that they may touch.
-  // The rows of either table are an odd number of 16-byte pieces apart: eight rows meet no bank twice.
+  // 2 kStepGroups bytes at any even place, its zero points kStepGroups bytes at any place: the aligned
+  // 16-byte pieces that they touch are copied.  The rows of either table are an odd number of pieces
+  // apart: eight rows meet no bank twice.
   static constexpr int kRows = 16 * MT * kSubs;
-  static constexpr int odd_pieces(int bytes) { return ((bytes + 15) / 16 | 1) * 16; }
-  static constexpr int kScaleWords = kStepGroups / 2 + 1, kScaleRow = odd_pieces(4 * kScaleWords);
-  static constexpr int kZeroWords = (kStepGroups + 2) / 4 + 1, kZeroRow = ZEROS ? odd_pieces(4 * kZeroWords) : 0;
+  static constexpr int kScalePieces = (14 + 2 * kStepGroups + 15) / 16, kScaleRow = (kScalePieces | 1) * 16;
+  static constexpr int kZeroPieces = (15 + kStepGroups + 15) / 16, kZeroRow = ZEROS ? (kZeroPieces | 1) * 16 : 0;
   static constexpr int kScaleAt = kMulPerTeam * MT * kTileBytes, kZeroAt = kScaleAt + kRows * kScaleRow;
   static constexpr int kStage = (kZeroAt + kRows * kZeroRow + 127) / 128 * 128;
   static constexpr int kPartial = MT * kTok * 16;                               // floats per warp and buffer
@@ -321,8 +317,6 @@ struct GemvKernel {
     const int64_t groups_total = p.E * p.N * KG;
     const uint8_t* const scales = reinterpret_cast<const uint8_t*>(p.scales);
     const uint32_t ring_at = smem_addr(ring);
-    const bool scale_pieces = kStepGroups % 8 == 0 && KG % 8 == 0 && reinterpret_cast<uintptr_t>(scales) % 16 == 0;
-    const bool zero_pieces = kStepGroups % 16 == 0 && KG % 16 == 0 && reinterpret_cast<uintptr_t>(p.zeros) % 16 == 0;
     // a row's pieces change places by its number: row r's piece i stands at i ^ (r & 7)
     const uint32_t code_at = ring_at + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));  // h odd: ^ 64
     Walk<kTok> walk;
@@ -331,8 +325,8 @@ struct GemvKernel {
     for (; walk.left > 0; walk.advance(p, col_tiles, teams)) {
       const int left = (int)min((int64_t)kItemCols, cols - (int64_t)walk.col * kItemCols);  // columns of this item
       const int64_t row0 = walk.tok.e * p.N + (int64_t)walk.col * kItemCols;
-      // a copied word may reach past the arrays' ends: a stage may name groups past a row's last
-      const bool near_end = row0 + (SWIGLU ? cols : 0) + kItemCols + kStepGroups >= p.E * p.N;
+      // a copied piece may reach past the arrays' ends: a stage may name groups past a row's last
+      const bool near_end = row0 + (SWIGLU ? cols : 0) + kItemCols + kStepGroups + 16 >= p.E * p.N;
       const uint8_t* code_src[MT][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -377,51 +371,31 @@ struct GemvKernel {
         }
         const int g0 = k0 / (32 * GB);
         const uint32_t scale_at = ring_at + stage * kStage + kScaleAt, zero_at = ring_at + stage * kStage + kZeroAt;
-        if (scale_pieces) {
-          constexpr int kPieces = kStepGroups / 8 ? kStepGroups / 8 : 1;
 #pragma unroll
-          for (int s0 = 0; s0 < kRows * kPieces; s0 += 32) {
-            const int s = s0 + lane, r = s / kPieces, q = s % kPieces;
-            if (s < kRows * kPieces && row_of(r) < left && g0 + 8 * q < KG)
-              copy16(scale_at + r * kScaleRow + 16 * q, scales + 2 * base(r) + 2 * (row_of(r) * KG + g0 + 8 * q));
-          }
-        } else {
-#pragma unroll
-          for (int s0 = 0; s0 < kRows * kScaleWords; s0 += 32) {
-            const int s = s0 + lane, r = s / kScaleWords, w = s % kScaleWords;
-            const int64_t b = base(r);
-            const int at = ((int)b & 1) + row_of(r) * KG + g0;  // from the aligned word that b is in
-            if (s < kRows * kScaleWords && row_of(r) < left && 2 * w < (at & 1) + kStepGroups) {
-              const uint8_t* const src = scales + (b >> 1) * 4 + ((at >> 1) + w) * 4;
-              if (near_end)
-                copy4(scale_at + r * kScaleRow + 4 * w, src, scales + 2 * groups_total, scales);
-              else
-                copy4(scale_at + r * kScaleRow + 4 * w, src);
-            }
+        for (int s0 = 0; s0 < kRows * kScalePieces; s0 += 32) {
+          const int s = s0 + lane, r = s / kScalePieces, q = s % kScalePieces;
+          const int64_t b = base(r);
+          const int at = ((int)b & 7) + row_of(r) * KG + g0;  // in scales, from the piece that b is in
+          if (s < kRows * kScalePieces && row_of(r) < left && 8 * q < (at & 7) + kStepGroups) {
+            const uint8_t* const src = scales + (b >> 3) * 16 + ((at >> 3) + q) * 16;
+            if (near_end)
+              copy16(scale_at + r * kScaleRow + 16 * q, src, scales + 2 * groups_total, scales);
+            else
+              copy16(scale_at + r * kScaleRow + 16 * q, src);
           }
         }
         if constexpr (ZEROS) {
-          if (zero_pieces) {
-            constexpr int kPieces = kStepGroups / 16 ? kStepGroups / 16 : 1;
 #pragma unroll
-            for (int s0 = 0; s0 < kRows * kPieces; s0 += 32) {
-              const int s = s0 + lane, r = s / kPieces, q = s % kPieces;
-              if (s < kRows * kPieces && row_of(r) < left && g0 + 16 * q < KG)
-                copy16(zero_at + r * kZeroRow + 16 * q, p.zeros + base(r) + (row_of(r) * KG + g0 + 16 * q));
-            }
-          } else {
-#pragma unroll
-            for (int s0 = 0; s0 < kRows * kZeroWords; s0 += 32) {
-              const int s = s0 + lane, r = s / kZeroWords, w = s % kZeroWords;
-              const int64_t b = base(r);
-              const int at = ((int)b & 3) + row_of(r) * KG + g0;
-              if (s < kRows * kZeroWords && row_of(r) < left && 4 * w < (at & 3) + kStepGroups) {
-                const uint8_t* const src = p.zeros + (b >> 2) * 4 + ((at >> 2) + w) * 4;
-                if (near_end)
-                  copy4(zero_at + r * kZeroRow + 4 * w, src, p.zeros + groups_total, p.zeros);
-                else
-                  copy4(zero_at + r * kZeroRow + 4 * w, src);
-              }
+          for (int s0 = 0; s0 < kRows * kZeroPieces; s0 += 32) {
+            const int s = s0 + lane, r = s / kZeroPieces, q = s % kZeroPieces;
+            const int64_t b = base(r);
+            const int at = ((int)b & 15) + row_of(r) * KG + g0;
+            if (s < kRows * kZeroPieces && row_of(r) < left && 16 * q < (at & 15) + kStepGroups) {
+              const uint8_t* const src = p.zeros + (b >> 4) * 16 + ((at >> 4) + q) * 16;
+              if (near_end)
+                copy16(zero_at + r * kZeroRow + 16 * q, src, p.zeros + groups_total, p.zeros);
+              else
+                copy16(zero_at + r * kZeroRow + 16 * q, src);
             }
           }
         }
@@ -470,7 +444,9 @@ struct GemvKernel {
     // x of kAhead blocks of the chunk at entry k, as it stands in memory, read one such part ahead
     constexpr int kAhead = NT == 1 ? 4 : 2, kParts = kChunk / 32 / kAhead;
     const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
-    int scale_odd[MT], zero_odd[MT];  // where the first group of its row of tile i stands within a word
+    // Where the first group of this lane's row of tile i stands within a piece, in bytes.  A further
+    // stage's first group is at least 8 on: the same place of a scale, maybe 8 bytes on of a zero point.
+    int scale_odd[MT], zero_odd[MT];
     auto read_x = [&](uint4 (&xv)[NT][kAhead], int k, int part, int blocks) {
       if constexpr (!XW)
 #pragma unroll
@@ -491,11 +467,11 @@ struct GemvKernel {
           if (jb && !both) break;
           const int jj = j + jb;
           uint32_t zl = Expand<XT>::zero(8), zh = zl;
-          // rows g and g + 8 start alike within a word
-          if (ZEROS) {
-            const uint8_t* zp = zero_row + stage + zero_odd[i] + 16 * i * kZeroRow + jj / GB;
-            zl = Expand<XT>::zero_of(zp[0]);
-            zh = Expand<XT>::zero_of(zp[8 * kZeroRow]);
+          if (ZEROS) {  // eight rows on, an odd KG moves the place by eight bytes
+            const uint8_t* zp = zero_row + stage + 16 * i * kZeroRow + jj / GB;
+            const int l = zero_odd[i] + (GB == 4 ? (k - kw * kChunk) >> 7 : 0), h = l + 8 * (KG & 1);
+            zl = Expand<XT>::zero_of(zp[l & 15]);
+            zh = Expand<XT>::zero_of(zp[8 * kZeroRow + (h & 15)]);
           }
           uint32_t lo[4], hi[4];
           expand8<XT>(words[2 * jb], zl, lo);
@@ -542,10 +518,10 @@ struct GemvKernel {
     for (; walk.left > 0; walk.advance(p, col_tiles, teams)) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        // further tiles of 16 rows: the same place
+        // rows 8 on, and further tiles of 16: the same place of a scale
         const int64_t row = walk.tok.e * p.N + (SWIGLU ? i * cols : 0) + (int64_t)walk.col * kItemCols + g;
-        scale_odd[i] = (int)(row & 1) * (KG & 1) * 2;
-        zero_odd[i] = (int)(row & 3) * KG & 3;
+        scale_odd[i] = ((int)(row & 7) * KG & 7) * 2;
+        zero_odd[i] = (int)(row & 15) * KG & 15;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -581,8 +581,8 @@ int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void* ys, int ys
  * [P5] "Why NVFP4 helps without FP4 hardware": the weight bytes are what a decode step reads).
  *   value[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
  *   codes   device [rows, K/2] bytes, q in 0..15, entry 2i in the low nibble, 16-byte aligned
- *   scales  device [rows, K/group], F16 or BF16 (scale_dtype), 4-byte aligned
- *   zeros   device [rows, K/group] bytes, 4-byte aligned, the low four bits are read; NULL: 8
+ *   scales  device [rows, K/group], F16 or BF16 (scale_dtype), 16-byte aligned
+ *   zeros   device [rows, K/group] bytes, 16-byte aligned, the low four bits are read; NULL: 8
  *           everywhere
  *   group   32, 64 or 128;  K % group == 0 */
 typedef struct {

@@ -70,7 +70,7 @@ def test_w4_refusals():
     assert q(G=16) == q(G=256) == q(G=0) == sp.ERR_UNSUPPORTED
     assert q(R=-1) == q(K=-128) == q(K=192) == sp.ERR_SHAPE
     assert q(z=1) == q(zp=16) == q(w=None) == q(c=None) == q(s=None) == sp.ERR_INVALID_ARG
-    assert q(w=24) == q(c=24) == q(s=17) == sp.ERR_ALIGN
+    assert q(w=24) == q(c=24) == q(s=24) == sp.ERR_ALIGN
     assert q(R=0, w=None, c=None, s=None) == sp.OK
     d = lambda op, K=256, dt=sp.F32, out=16: _raw("sp24_dequantize_w4", ctypes.byref(op), 4, K, dt, out, None)  # noqa: E731
     assert d(_op(scale=sp.F32)) == d(_op(), dt=sp.NVFP4) == sp.ERR_DTYPE
@@ -90,7 +90,7 @@ def test_gemv_w4_refusals(grouped):
     assert f(act=2) == f(x=None) == f(y=None) == f(_op(codes=None)) == f(_op(scales=None)) == sp.ERR_INVALID_ARG
     assert f(_op(group=96)) == f(K=2**24 + 128) == f(M=2**31) == f(N=2**31) == sp.ERR_UNSUPPORTED
     assert f(K=192) == f(K=-128) == f(M=-1) == f(N=-1) == f(N=5, act=1) == sp.ERR_SHAPE
-    assert f(x=24) == f(y=18) == f(_op(codes=24)) == f(_op(scales=18)) == f(_op(zeros=18)) == sp.ERR_ALIGN
+    assert f(x=24) == f(y=18) == f(_op(codes=24)) == f(_op(scales=24)) == f(_op(zeros=24)) == sp.ERR_ALIGN
     assert f(M=0, x=None, y=None) == f(N=0, y=None) == sp.OK
     if grouped:
         assert f(E=0) == sp.ERR_SHAPE and f(off=None) == sp.ERR_INVALID_ARG and f(off=18) == sp.ERR_ALIGN

@@ -9,6 +9,11 @@ Pipeline ([P1] "NVFP4 vs 2:4 sparse: where the other half of the petaflop went",
 Hardware"):
 
     check_24 -> prune_compress_24 -> quantize_nvfp4 -> gemm_dense / gemm_sparse24
+
+Routed feed-forward around gemm_grouped / moe_block, and its single-token form with 4-bit weights:
+
+    moe_route -> moe_sort -> gemm_grouped or gemv_w4_grouped -> moe_unsort, each with its _backward
+    (moe_sort_backward, moe_unsort_backward, moe_route_backward) where it is differentiable
 """
 from __future__ import annotations
 
@@ -862,7 +867,7 @@ def _placed(impl):
             t = t.codes
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
-        if stream is None and t.get_device() == torch.cuda.current_device():
+        if stream is None and t.get_device() == _current_device():
             return impl(*args, **kw)
         if stream is not None and stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
@@ -871,15 +876,20 @@ def _placed(impl):
     return call
 
 
-# the current stream of a device, as the runtime's own handle
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the current device, and a device's current stream as the runtime's own handle, without the
+# initialisation check of torch.cuda's functions (a CUDA tensor is at hand)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _arg(t, name: str, dev: int, shape, *dtypes) -> int:
     """The address of an argument that has to be contiguous, on device `dev`, and of this shape and
     type."""
-    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.get_device() == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise ValueError(f"{name} must be a tensor on cuda:{dev}")
     if t.dtype not in dtypes:

@@ -196,7 +196,7 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   const int st = check_w4(N, K, w->group);
   if (st) return st;
   if (M < 0 || E < 1 || (act == SP24_ACT_SWIGLU && N % 2)) return SP24_ERR_SHAPE;
-  if (M > INT32_MAX || E > INT32_MAX || N > INT32_MAX || K > (1 << 24)) return SP24_ERR_UNSUPPORTED;
+  if (M > INT32_MAX || E > (1 << 20) || N > INT32_MAX || K > (1 << 24)) return SP24_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return SP24_OK;
   const int64_t cols = act == SP24_ACT_SWIGLU ? N / 2 : N;
   const int yb = elem_bytes(y_dtype);

@@ -118,72 +118,89 @@ __device__ __forceinline__ void expand8(uint32_t word, uint32_t zero, uint32_t (
   out[3] = X::fma2(up & 0x00f000f0u, X::kHigh, zero);
 }
 
-// The token tiles of all experts, in expert order: expert e has ceil(rows of e / step) of them.
+// The token tiles of all experts, in expert order: expert e has ceil(rows of e / STEP) of them.
 // Everything here is computed by a whole warp together.
 struct TokenTile {
   int64_t e, m0, m1;  // expert, first row, end of the expert's rows
 };
 
-__device__ __forceinline__ int64_t expert_rows(const GemvW4& p, int64_t e, int64_t& first, int64_t& end) {
-  first = max(0, p.offsets[e]);
-  end = min(p.M, (int64_t)p.offsets[e + 1]);
-  return max((int64_t)0, end - first);
+// Expert e's rows, [first, end); none past the last expert.
+__device__ __forceinline__ void expert_rows(const GemvW4& p, int e, int& first, int& end) {
+  first = end = 0;
+  if (e < p.E) {
+    first = max(0, p.offsets[e]);
+    end = max(first, min((int)p.M, p.offsets[e + 1]));
+  }
 }
 
-__device__ __forceinline__ int64_t warp_scan(int64_t v) {
+constexpr int kLook = 8;  // loads of 32 experts' offsets in flight
+
+// f(e0, tiles of expert e0 + lane) for 32 experts after another, until it says stop.
+template <int STEP, typename F>
+__device__ __forceinline__ void each_32_experts(const GemvW4& p, F f) {
   const int lane = threadIdx.x & 31;
+  for (int e0 = 0; e0 < p.E; e0 += 32 * kLook) {
+    int tiles[kLook];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(kFull, v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-
-// The number of token tiles; lane l's run of ceil(E / 32) experts has those before `upto`.
-__device__ __forceinline__ int64_t count_tiles(const GemvW4& p, int step, int64_t& mine, int64_t& upto) {
-  const int lane = threadIdx.x & 31;
-  const int64_t per = (p.E + 31) / 32;
-  int64_t a, b;
-  mine = 0;
-  for (int64_t i = lane * per; i < min(p.E, (lane + 1) * per); ++i) mine += (expert_rows(p, i, a, b) + step - 1) / step;
-  upto = warp_scan(mine);
-  return __shfl_sync(kFull, upto, 31);
-}
-
-// Tile number `tile`, given count_tiles' values.
-__device__ __forceinline__ TokenTile find_tile(const GemvW4& p, int step, int64_t mine, int64_t upto, int64_t tile) {
-  const int lane = threadIdx.x & 31;
-  const int64_t per = (p.E + 31) / 32;
-  const int who = __ffs(__ballot_sync(kFull, upto > tile)) - 1;
-  tile -= __shfl_sync(kFull, upto - mine, who);
-  const int64_t end = min(p.E, (who + 1) * per);
-  for (int64_t i0 = who * per; i0 < end; i0 += 32) {
-    int64_t a = 0, b = 0;
-    const int64_t n = i0 + lane < end ? (expert_rows(p, i0 + lane, a, b) + step - 1) / step : 0;
-    const int64_t s = warp_scan(n);
-    const unsigned hit = __ballot_sync(kFull, s > tile);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      const int64_t first = __shfl_sync(kFull, a, l), before = __shfl_sync(kFull, s - n, l);
-      return {i0 + l, first + (tile - before) * step, __shfl_sync(kFull, b, l)};
+    for (int k = 0; k < kLook; ++k) {
+      int first, end;
+      expert_rows(p, e0 + 32 * k + lane, first, end);
+      tiles[k] = (end - first + STEP - 1) / STEP;
     }
-    tile -= __shfl_sync(kFull, s, 31);
+#pragma unroll
+    for (int k = 0; k < kLook; ++k)
+      if (f(e0 + 32 * k, tiles[k])) return;
   }
-  return {0, 0, 0};  // not reached: tile is below the count
+}
+
+template <int STEP>
+__device__ __forceinline__ int count_tiles(const GemvW4& p) {
+  int mine = 0;
+  each_32_experts<STEP>(p, [&](int, int tiles) {
+    mine += tiles;
+    return false;
+  });
+  return __reduce_add_sync(kFull, mine);
+}
+
+// Tile number `tile`, which is below the count.
+template <int STEP>
+__device__ __forceinline__ TokenTile find_tile(const GemvW4& p, int tile) {
+  const int lane = threadIdx.x & 31;
+  TokenTile t{0, 0, 0};
+  each_32_experts<STEP>(p, [&](int e0, int tiles) {
+    const int here = __reduce_add_sync(kFull, tiles);
+    if (tile >= here) {
+      tile -= here;
+      return false;
+    }
+    int upto = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, upto, d);
+      if (lane >= d) upto += o;
+    }
+    const int l = __ffs(__ballot_sync(kFull, upto > tile)) - 1;
+    int first, end;
+    expert_rows(p, e0 + l, first, end);
+    t = {e0 + l, first + (tile - __shfl_sync(kFull, upto - tiles, l)) * STEP, end};
+    return true;
+  });
+  return t;
 }
 
 // The tile after t (there is one).
-__device__ __forceinline__ TokenTile next_tile(const GemvW4& p, int step, const TokenTile& t) {
-  if (t.m0 + step < t.m1) return {t.e, t.m0 + step, t.m1};
+template <int STEP>
+__device__ __forceinline__ TokenTile next_tile(const GemvW4& p, const TokenTile& t) {
+  if (t.m0 + STEP < t.m1) return {t.e, t.m0 + STEP, t.m1};
   const int lane = threadIdx.x & 31;
-  for (int64_t e = t.e + 1; e < p.E; e += 32) {
-    int64_t a = 0, b = 0;
-    const bool some = e + lane < p.E && expert_rows(p, e + lane, a, b) > 0;
-    const unsigned hit = __ballot_sync(kFull, some);
+  for (int e = (int)t.e + 1; e < p.E; e += 32) {
+    int first, end;
+    expert_rows(p, e + lane, first, end);
+    const unsigned hit = __ballot_sync(kFull, first < end);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      return {e + l, __shfl_sync(kFull, a, l), __shfl_sync(kFull, b, l)};
+      return {e + l, __shfl_sync(kFull, first, l), __shfl_sync(kFull, end, l)};
     }
   }
   return t;  // not reached
@@ -201,13 +218,12 @@ struct Walk {
 
   __device__ __forceinline__ void start(const GemvW4& p, int col_tiles, int team, int teams) {
     if (p.offsets) {
-      int64_t mine, upto;
-      const int64_t all = count_tiles(p, STEP, mine, upto) * col_tiles;
+      const int64_t all = (int64_t)count_tiles<STEP>(p) * col_tiles;
       const int64_t first = all * team / teams;
       left = (int)(all * (team + 1) / teams - first);
       if (left <= 0) return;
       col = (int)(first % col_tiles);
-      tok = find_tile(p, STEP, mine, upto, first / col_tiles);
+      tok = find_tile<STEP>(p, (int)(first / col_tiles));
     } else {
       const int tiles = (int)((p.M + STEP - 1) / STEP), all = tiles * col_tiles;
       item = team;
@@ -224,7 +240,7 @@ struct Walk {
     if (p.offsets) {
       if (++col == col_tiles) {
         col = 0;
-        tok = next_tile(p, STEP, tok);
+        tok = next_tile<STEP>(p, tok);
       }
     } else {
       item += teams;
@@ -444,8 +460,8 @@ struct GemvKernel {
     // x of kAhead blocks of the chunk at entry k, as it stands in memory, read one such part ahead
     constexpr int kAhead = NT == 1 ? 4 : 2, kParts = kChunk / 32 / kAhead;
     const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
-    // Where the first group of this lane's row of tile i stands within a piece, in bytes.  A further
-    // stage's first group is at least 8 on: the same place of a scale, maybe 8 bytes on of a zero point.
+    // Where the first group of this lane's row of tile i stands within a piece, in bytes; a further stage
+    // moves that on unless its groups fill pieces.
     int scale_odd[MT], zero_odd[MT];
     auto read_x = [&](uint4 (&xv)[NT][kAhead], int k, int part, int blocks) {
       if constexpr (!XW)
@@ -469,7 +485,7 @@ struct GemvKernel {
           uint32_t zl = Expand<XT>::zero(8), zh = zl;
           if (ZEROS) {  // eight rows on, an odd KG moves the place by eight bytes
             const uint8_t* zp = zero_row + stage + 16 * i * kZeroRow + jj / GB;
-            const int l = zero_odd[i] + (GB == 4 ? (k - kw * kChunk) >> 7 : 0), h = l + 8 * (KG & 1);
+            const int l = zero_odd[i] + (kStepGroups % 16 ? (k - kw * kChunk) / (32 * GB) : 0), h = l + 8 * (KG & 1);
             zl = Expand<XT>::zero_of(zp[l & 15]);
             zh = Expand<XT>::zero_of(zp[8 * kZeroRow + (h & 15)]);
           }
@@ -494,7 +510,8 @@ struct GemvKernel {
             mma16816<XT>(acc[i][n], a1, b.z, b.w);
           }
           if ((jj + 1) % GB == 0) {
-            const uint8_t* sp = scale_row + stage + scale_odd[i] + 16 * i * kScaleRow + 2 * (jj / GB);
+            const int from = kStepGroups % 8 ? (scale_odd[i] + (k - kw * kChunk) / (16 * GB)) & 15 : scale_odd[i];
+            const uint8_t* sp = scale_row + stage + from + 16 * i * kScaleRow + 2 * (jj / GB);
             const uint32_t l = *reinterpret_cast<const uint16_t*>(sp);
             const uint32_t h = *reinterpret_cast<const uint16_t*>(sp + 8 * kScaleRow);
             const float sl = p.scale_dtype == SP24_BF16 ? W4Half<SP24_BF16>::get(l) : W4Half<SP24_F16>::get(l);

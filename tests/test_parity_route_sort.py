@@ -257,7 +257,7 @@ def test_sort(dtype, T, k, E, H):
     sp.last_device_error()
 
 
-@pytest.mark.parametrize("T,k,E", [(5000, 2, 9), (4096, 10, 512), (3001, 5, 1030), (60000, 1, 3), (20011, 8, 128)])
+@pytest.mark.parametrize("T,k,E", [(5000, 2, 9), (4096, 10, 512), (1024, 2, 7), (1025, 2, 7), (300, 2, 20000), (9000, 1, 30000), (3001, 5, 1030), (60000, 1, 3), (20011, 8, 128)])
 def test_sort_many(T, k, E):
     """Many entries: skewed experts (some empty, one with a third of all), padded tokens."""
     rng = np.random.default_rng(E)
@@ -436,12 +436,13 @@ def test_refusals():
             call()
 
 
-def test_other_stream_and_graph():
+@pytest.mark.parametrize("T", [300, 2500])
+def test_other_stream_and_graph(T):
     """On a stream of its own, and captured and replayed on new inputs: the results of plain calls."""
     g = torch.Generator().manual_seed(9)
     E, k, H = 40, 4, 96
-    logits = torch.randn(500, E, generator=g).cuda()
-    x = torch.randn(500, H, generator=g).bfloat16().cuda()
+    logits = torch.randn(T, E, generator=g).cuda()
+    x = torch.randn(T, H, generator=g).bfloat16().cuda()
 
     def chain(stream=None):
         routing, w = sp.moe_route(logits, k, stream=stream)
@@ -460,9 +461,35 @@ def test_other_stream_and_graph():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         held = chain()
-    logits.copy_(torch.randn(500, E, generator=g))
-    x.copy_(torch.randn(500, H, generator=g))
+    logits.copy_(torch.randn(T, E, generator=g))
+    x.copy_(torch.randn(T, H, generator=g))
     graph.replay()
     again = [t.clone() for t in held]
     assert all(torch.equal(a, b) for a, b in zip(again, chain()))
     _cuda_ok()
+
+
+def test_sorts_at_once_on_two_streams():
+    """Sorts that overlap, each with a workspace of its own."""
+    rs = [torch.from_numpy(np.random.default_rng(s).integers(0, 30, (3000, 3)).astype(np.int32)).cuda() for s in range(2)]
+    want = [sp.moe_sort_tables(r, 30) for r in rs]
+    streams = [torch.cuda.Stream() for _ in rs]
+    torch.cuda.synchronize()
+    got = [(i, sp.moe_sort_tables(rs[i], 30, stream=streams[i])) for _ in range(20) for i in range(2)]
+    _cuda_ok()
+    assert all(torch.equal(a, b) for i, t in got for a, b in zip(t[1:], want[i][1:]))
+
+
+def test_route_weights_of_one_expert_and_extremes():
+    """One expert; logits at the type's ends (differences that overflow to infinity included)."""
+    l = torch.tensor([[3.0e38, -3.0e38, 1.0, 3.0e38], [-3.0e38, -3.0e38, -3.0e38, -3.0e38]], device="cuda")
+    ids, w = sp.moe_route(l, 2)
+    assert ids.tolist() == [[0, 3], [0, 1]] and w.tolist() == [[0.5, 0.5], [0.5, 0.5]]
+    _, w = sp.moe_route(l, 2, sp.ROUTE_SIGMOID, False)
+    assert w.tolist() == [[1.0, 1.0], [0.0, 0.0]]
+    ids, w = sp.moe_route(l, 2, sp.ROUTE_SIGMOID, True)  # a sum of 0 leaves weights of 0
+    assert w.tolist() == [[0.5, 0.5], [0.0, 0.0]]
+    d = sp.moe_route_backward(torch.ones(2, 2, device="cuda"), l, ids, sp.ROUTE_SIGMOID, True)
+    assert not d.any()
+    ids, w = sp.moe_route(l[:, :1].contiguous(), 1, sp.ROUTE_SOFTMAX, False)
+    assert ids.tolist() == [[0], [0]] and w.tolist() == [[1.0], [1.0]]

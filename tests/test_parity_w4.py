@@ -211,6 +211,37 @@ def test_gemv_swiglu(M, F, K, G, dtype):
     _cuda_ok()
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 70, 256), (3, 129, 384), (8, 33, 512), (11, 65, 512), (2, 47, 640), (8, 50, 16512),
+                                   (16, 37, 9088), (20, 48, 1152), (1, 2400, 1920)])
+def test_gemv_paths(M, N, K, G, zeros):
+    """One or two chunks of K, an x that does not fit shared memory, two tiles of rows, odd numbers of
+    groups (rows of scales and zero points at every place within sixteen bytes)."""
+    x = torch.randn(M, K, generator=_gen(M + K)).half().cuda()
+    w = random_w4(N, K, G, zeros, torch.float16, N)
+    y = sp.gemv_w4(x, w)
+    assert_close(y, *product_ref(x, w))
+    if N % 2 == 0:
+        assert_close(sp.gemv_w4(x, w, sp.ACT_SWIGLU), *swiglu_ref(*product_ref(x, w)))
+    _cuda_ok()
+
+
+def test_gemv_two_streams_at_once():
+    """Calls that overlap share nothing: the bits are those of calls made alone."""
+    x = torch.randn(4, 2048, generator=_gen(1)).bfloat16().cuda()
+    ws = [random_w4(3000, 2048, 64, True, torch.bfloat16, s) for s in range(2)]
+    want = [sp.gemv_w4(x, w) for w in ws]
+    streams = [torch.cuda.Stream() for _ in ws]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (w, st) in enumerate(zip(ws, streams)):
+            got[i].append(sp.gemv_w4(x, w, stream=st))
+    _cuda_ok()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+
+
 def test_gemv_scales_of_the_other_type():
     x = torch.randn(4, 256, generator=_gen(0)).bfloat16().cuda()
     w = random_w4(50, 256, 64, True, torch.float16, 1)
@@ -284,7 +315,8 @@ def _grouped_ref(x, w, offsets, E, act):
 @pytest.mark.parametrize("counts,N,K,G,zeros,dtype", [
     ([1], 2, 32, 32, False, torch.bfloat16), ([0, 3, 0, 1, 8, 0], 48, 128, 64, True, torch.float16),
     ([9, 17, 1, 0, 40], 34, 256, 128, False, torch.bfloat16), ([0, 0, 0, 5], 130, 1056, 32, True, torch.bfloat16),
-    ([2] * 70, 32, 96, 32, False, torch.float16), ([0] * 300 + [1, 0, 16] + [0] * 50, 20, 512, 128, True, torch.bfloat16)])
+    ([2] * 70, 32, 96, 32, False, torch.float16), ([3, 0, 1, 9], 70, 512, 128, True, torch.bfloat16),
+    ([1] * 40, 66, 2048, 64, False, torch.float16), ([30, 50], 48, 1184, 32, True, torch.bfloat16), ([0] * 300 + [1, 0, 16] + [0] * 50, 20, 512, 128, True, torch.bfloat16)])
 def test_gemv_grouped(act, counts, N, K, G, zeros, dtype):
     E, live = len(counts), sum(counts)
     offsets = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32).cuda()

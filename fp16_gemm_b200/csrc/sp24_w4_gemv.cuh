@@ -438,13 +438,18 @@ struct GemvKernel {
     uint8_t* const x_all = smem + kFixed;
     if (XW) {
       const int pieces = K / 8;
-      for (int m = 0; m < (int)p.M; ++m)
-        for (int j = threadIdx.x; j < pieces; j += 32 * kMulWarps) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)m * pieces + j);
-          *reinterpret_cast<uint4*>(x_all + m * x_stride(K) + 16 * j) =
-              make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                         __byte_perm(v.y, v.w, 0x7632));
-        }
+      for (int j = threadIdx.x; j < pieces; j += 32 * kMulWarps) {
+        uint4 v[kTok];  // every row's loads in flight together
+#pragma unroll
+        for (int m = 0; m < kTok; ++m)
+          if (m < (int)p.M) v[m] = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)m * pieces + j);
+#pragma unroll
+        for (int m = 0; m < kTok; ++m)
+          if (m < (int)p.M)
+            *reinterpret_cast<uint4*>(x_all + m * x_stride(K) + 16 * j) =
+                make_uint4(__byte_perm(v[m].x, v[m].z, 0x5410), __byte_perm(v[m].x, v[m].z, 0x7632),
+                           __byte_perm(v[m].y, v[m].w, 0x5410), __byte_perm(v[m].y, v[m].w, 0x7632));
+      }
       asm volatile("bar.sync %0, %1;" ::"r"(1 + kTeams), "r"(32 * kMulWarps) : "memory");
     }
 

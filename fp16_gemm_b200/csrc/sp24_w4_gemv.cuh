@@ -133,30 +133,45 @@ __device__ __forceinline__ void expert_rows(const GemvW4& p, int e, int& first, 
   }
 }
 
-constexpr int kLook = 8;  // loads of 32 experts' offsets in flight
-
-// f(e0, tiles of expert e0 + lane) for 32 experts after another, until it says stop.
-template <int STEP, typename F>
-__device__ __forceinline__ void each_32_experts(const GemvW4& p, F f) {
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int warp_scan(int v) {
   const int lane = threadIdx.x & 31;
-  for (int e0 = 0; e0 < p.E; e0 += 32 * kLook) {
-    int tiles[kLook];
 #pragma unroll
-    for (int k = 0; k < kLook; ++k) {
-      int first, end;
-      expert_rows(p, e0 + 32 * k + lane, first, end);
-      tiles[k] = (end - first + STEP - 1) / STEP;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kFull, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// The tiles of experts 32 b .. 32 b + 31.
+template <int STEP>
+__device__ __forceinline__ int block_tiles(const GemvW4& p, int b) {
+  int first, end;
+  expert_rows(p, 32 * b + (threadIdx.x & 31), first, end);
+  return __reduce_add_sync(kFull, (end - first + STEP - 1) / STEP);
+}
+
+// A CTA's warps share the counting: `table` holds block_tiles of the first kBlocks blocks.
+constexpr int kBlocks = 192;
+
+template <int STEP, typename F>
+__device__ __forceinline__ void each_32_blocks(const GemvW4& p, const int* table, F f) {
+  const int lane = threadIdx.x & 31, blocks = (int)((p.E + 31) / 32);
+  for (int b0 = 0; b0 < blocks; b0 += 32) {
+    int mine = b0 + lane < min(blocks, kBlocks) ? table[b0 + lane] : 0;
+    for (int b = max(b0, kBlocks); b < min(blocks, b0 + 32); ++b) {  // experts that the table has no room for
+      const int s = block_tiles<STEP>(p, b);
+      if (b == b0 + lane) mine = s;
     }
-#pragma unroll
-    for (int k = 0; k < kLook; ++k)
-      if (f(e0 + 32 * k, tiles[k])) return;
+    if (f(b0, mine)) return;
   }
 }
 
 template <int STEP>
-__device__ __forceinline__ int count_tiles(const GemvW4& p) {
+__device__ __forceinline__ int count_tiles(const GemvW4& p, const int* table) {
   int mine = 0;
-  each_32_experts<STEP>(p, [&](int, int tiles) {
+  each_32_blocks<STEP>(p, table, [&](int, int tiles) {
     mine += tiles;
     return false;
   });
@@ -165,25 +180,26 @@ __device__ __forceinline__ int count_tiles(const GemvW4& p) {
 
 // Tile number `tile`, which is below the count.
 template <int STEP>
-__device__ __forceinline__ TokenTile find_tile(const GemvW4& p, int tile) {
+__device__ __forceinline__ TokenTile find_tile(const GemvW4& p, const int* table, int tile) {
   const int lane = threadIdx.x & 31;
   TokenTile t{0, 0, 0};
-  each_32_experts<STEP>(p, [&](int e0, int tiles) {
+  // the lane whose tiles the wanted one is among; the tiles before that lane's are taken off
+  auto pick = [&](int tiles) {
+    const int upto = warp_scan(tiles), l = __ffs(__ballot_sync(kFull, upto > tile)) - 1;
+    if (l >= 0) tile -= __shfl_sync(kFull, upto - tiles, l);
+    return l;
+  };
+  each_32_blocks<STEP>(p, table, [&](int b0, int tiles) {
     const int here = __reduce_add_sync(kFull, tiles);
     if (tile >= here) {
       tile -= here;
       return false;
     }
-    int upto = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(kFull, upto, d);
-      if (lane >= d) upto += o;
-    }
-    const int l = __ffs(__ballot_sync(kFull, upto > tile)) - 1;
+    const int e0 = 32 * (b0 + pick(tiles));
     int first, end;
-    expert_rows(p, e0 + l, first, end);
-    t = {e0 + l, first + (tile - __shfl_sync(kFull, upto - tiles, l)) * STEP, end};
+    expert_rows(p, e0 + lane, first, end);
+    const int l = pick((end - first + STEP - 1) / STEP);
+    t = {e0 + l, __shfl_sync(kFull, first, l) + tile * STEP, __shfl_sync(kFull, end, l)};
     return true;
   });
   return t;
@@ -216,14 +232,14 @@ struct Walk {
   int col;    // column tile
   TokenTile tok;
 
-  __device__ __forceinline__ void start(const GemvW4& p, int col_tiles, int team, int teams) {
+  __device__ __forceinline__ void start(const GemvW4& p, const int* table, int col_tiles, int team, int teams) {
     if (p.offsets) {
-      const int64_t all = (int64_t)count_tiles<STEP>(p) * col_tiles;
+      const int64_t all = (int64_t)count_tiles<STEP>(p, table) * col_tiles;
       const int64_t first = all * team / teams;
       left = (int)(all * (team + 1) / teams - first);
       if (left <= 0) return;
       col = (int)(first % col_tiles);
-      tok = find_tile<STEP>(p, (int)(first / col_tiles));
+      tok = find_tile<STEP>(p, table, (int)(first / col_tiles));
     } else {
       const int tiles = (int)((p.M + STEP - 1) / STEP), all = tiles * col_tiles;
       item = team;
@@ -288,7 +304,9 @@ struct GemvKernel {
   static constexpr int kScaleAt = kMulPerTeam * MT * kTileBytes, kZeroAt = kScaleAt + kRows * kScaleRow;
   static constexpr int kStage = (kZeroAt + kRows * kZeroRow + 127) / 128 * 128;
   static constexpr int kPartial = MT * kTok * 16;                               // floats per warp and buffer
-  static constexpr int kBarriers = 1024;                                        // bytes
+  // The front of shared memory: the barriers, then the experts' tile counts.
+  static constexpr int kTableAt = 256, kBarriers = 1024;
+  static_assert(kTeams * S * 16 <= kTableAt && kTableAt + 4 * kBlocks <= kBarriers);
   static constexpr int kRing = kBarriers + 2 * kMulWarps * kPartial * 4;
   static constexpr int kFixed = kRing + kTeams * S * kStage;
 
@@ -308,13 +326,16 @@ struct GemvKernel {
       }
       tc::fence_mbar_init();
     }
+    int* const table = reinterpret_cast<int*>(smem + kTableAt);
+    if (p.offsets)
+      for (int b = warp; b < min((int)((p.E + 31) / 32), kBlocks); b += kMulWarps + kTeams) table[b] = block_tiles<kTok>(p, b);
     __syncthreads();
     const bool copies = warp >= kMulWarps;
     const int in_cta = copies ? warp - kMulWarps : warp / kMulPerTeam;
     const int team = in_cta * gridDim.x + blockIdx.x, teams = gridDim.x * kTeams;
     uint8_t* const ring = smem + kRing + in_cta * (S * kStage);
     if (copies)
-      copy(p, ring, bars + 2 * S * in_cta, team, teams);
+      copy(p, table, ring, bars + 2 * S * in_cta, team, teams);
     else
       multiply_all(p, smem, ring, bars + 2 * S * in_cta, warp, in_cta, team, teams);
   }
@@ -325,7 +346,7 @@ struct GemvKernel {
   }
 
   // ---- the copying warp: lane l copies piece l & 7 of rows (l >> 3) + 4 h of each of the four chunks
-  static __device__ __forceinline__ void copy(const GemvW4& p, uint8_t* ring, uint64_t* bars, int team, int teams) {
+  static __device__ __forceinline__ void copy(const GemvW4& p, const int* table, uint8_t* ring, uint64_t* bars, int team, int teams) {
     const int lane = threadIdx.x & 31;
     const int64_t cols = columns(p);
     const int col_tiles = column_tiles(p);
@@ -336,9 +357,16 @@ struct GemvKernel {
     // a row's pieces change places by its number: row r's piece i stands at i ^ (r & 7)
     const uint32_t code_at = ring_at + (lane >> 3) * 128 + 16 * ((lane & 7) ^ (lane >> 3));  // h odd: ^ 64
     Walk<kTok> walk;
-    walk.start(p, col_tiles, team, teams);
+    walk.start(p, table, col_tiles, team, teams);
     int stage = 0, round = 0;
+    int64_t near_row = -1;  // first row of x of the tile that was last brought to L1
     for (; walk.left > 0; walk.advance(p, col_tiles, teams)) {
+      if (!XW && walk.tok.m0 != near_row) {  // x of a new token tile: into L1 ahead of the multiplying warps
+        near_row = walk.tok.m0;
+        const uint8_t* const x = reinterpret_cast<const uint8_t*>(p.x) + near_row * K * 2;
+        for (int64_t at = 128 * lane; at < (int64_t)walk.rows() * K * 2; at += 128 * 32)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(x + at));
+      }
       const int left = (int)min((int64_t)kItemCols, cols - (int64_t)walk.col * kItemCols);  // columns of this item
       const int64_t row0 = walk.tok.e * p.N + (int64_t)walk.col * kItemCols;
       // a copied piece may reach past the arrays' ends: a stage may name groups past a row's last
@@ -454,7 +482,7 @@ struct GemvKernel {
     }
 
     Walk<kTok> walk;
-    walk.start(p, col_tiles, team, teams);
+    walk.start(p, reinterpret_cast<const int*>(smem + kTableAt), col_tiles, team, teams);
     // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4); block j + 2 n: ^ 32 n
     const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
     const uint32_t lm_at = smem_addr(ring) + in_team * (MT * kTileBytes) + lm_row * 128 + 16 * ((lane >> 4) ^ (lane & 7));

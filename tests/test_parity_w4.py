@@ -316,7 +316,8 @@ def _grouped_ref(x, w, offsets, E, act):
     ([1], 2, 32, 32, False, torch.bfloat16), ([0, 3, 0, 1, 8, 0], 48, 128, 64, True, torch.float16),
     ([9, 17, 1, 0, 40], 34, 256, 128, False, torch.bfloat16), ([0, 0, 0, 5], 130, 1056, 32, True, torch.bfloat16),
     ([2] * 70, 32, 96, 32, False, torch.float16), ([3, 0, 1, 9], 70, 512, 128, True, torch.bfloat16),
-    ([1] * 40, 66, 2048, 64, False, torch.float16), ([30, 50], 48, 1184, 32, True, torch.bfloat16), ([0] * 300 + [1, 0, 16] + [0] * 50, 20, 512, 128, True, torch.bfloat16)])
+    ([1] * 40, 66, 2048, 64, False, torch.float16), ([30, 50], 48, 1184, 32, True, torch.bfloat16), ([0] * 300 + [1, 0, 16] + [0] * 50, 20, 512, 128, True, torch.bfloat16),
+    ([0, 0, 1] * 900 + [0] * 4000 + [2, 9, 0, 0, 1] + [0] * 90, 2, 64, 64, False, torch.float16)])
 def test_gemv_grouped(act, counts, N, K, G, zeros, dtype):
     E, live = len(counts), sum(counts)
     offsets = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32).cuda()

@@ -11,6 +11,9 @@
 // of "largest one left, take it away" (T = 4096, E = 512, topk = 10: 5.4 against 9.0 us), which remain
 // for rows whose ties leave more than 32, and for E <= 64, where a round is cheap (T = 16384, E = 64,
 // topk = 8: 7.8 against 8.6 us).
+//
+// Bound by instruction issue and the launch: the logits of 4096 tokens over 512 experts are 8.4 MB, 1.3 us at
+// the copy rate; forward 5.5 us, gradient 3.9 us (4.7 where it is dense).
 #include "sp24_internal.cuh"
 
 namespace sp24 {

@@ -39,7 +39,8 @@ __device__ __forceinline__ uint32_t pair_bits(T v) {
 // nearest integer to 15 clamp(w / (15 s) + (z + 2^-16) / 15, 0, 1), which is within 2^-17 of
 // clamp(w / s + z + 2^-16, 0, 15): so it is that of the exact value, and an exact border goes up.
 //
-// Bound by instruction issue before HBM if done plainly, so the arithmetic is cut to four
+// Bound by instruction issue before HBM if done plainly (74 us for [12288, 5120] bf16, whose bytes take 24
+// at the copy rate; 26 us as it is, 29 with zero points), so the arithmetic is cut to four
 // instructions an entry: unpacking, one saturating fma (the clamp is its saturation), one fma that
 // adds 1.5 * 2^23 (whose last place is 1, which rounds to the integer), and one integer
 // multiply-add that joins the codes with the constant's bits still in them; their sum is
@@ -128,7 +129,8 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* __restric
 }
 
 // Eight codes per thread and turn, four turns in flight.  Where the output has the scales' type, q - z
-// (exact) times s is one multiplication in that type, which rounds once.
+// (exact) times s is one multiplication in that type, which rounds once: [12288, 5120] to bf16 takes 26 us
+// (24 at the copy rate), against 44 with conversions to fp32 and back.
 template <int DT, int ST>
 __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __restrict__ codes,
                                                             const uint16_t* __restrict__ scales,

@@ -273,12 +273,23 @@ struct Walk {
 // copies (cp.async, S stages of four chunks of 256 entries ahead, across the items' borders), four
 // multiply, each a chunk of every four; mbarriers tell the stages full and empty.  The four chunks
 // follow each other along K (WK 4), or, where K has no more than two, pairs of them along the columns
-// (WK 2).  The partial sums of the warps that share K meet in shared memory in a fixed order, in two buffers
-// that take turns, so one barrier of the team per item is enough.
+// (WK 2).  The partial sums of the warps that share K meet in shared memory in a fixed order, in two
+// buffers that take turns, so one barrier of the team per item is enough.
 //
 // An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of a 32-entry block
 // of rows g and g + 8; the MMA may sum K in any order, so the pairs that expand8 gives are fed as
 // they come, with x's pairs picked alike.  A group's sum is scaled in fp32.
+//
+// What bounds it: the bytes of codes and scales for large matrices (one token through [151936, 4096],
+// groups of 128: 62 us, 5.2 TB/s, 0.79 of the copy rate), with instruction issue close behind: a chunk of 16
+// rows, 2 KB, takes about 190 instructions of products proper, and an SM has 88 cycles for it at that
+// rate.  Hence warps of their own for the copies (68 against 74 us with every warp copying for itself:
+// no registers are left for its addresses), chunks of 256 instead of 128 entries, expand8 (74 against
+// 80 us with the codes or-ed into 2^7 and a subtraction), and tables copied per stage of four chunks
+// (groups of 32 with zero points: 86 against 146 us with a row's few bytes copied per chunk).  Small
+// matrices are bound by the launch, the first loads and a warp's own latency through its few chunks
+// ([5120, 5120]: 7 us, floor 2.1).  Experts (8 tokens over 10 of 512, SwiGLU, [1024, 2048] each: 25 us, 3.3 TB/s)
+// spend half of their instructions between items of two chunks a warp.
 //
 // XW: x stands in shared memory whole, its pairs picked when it is brought there; otherwise (experts,
 // or a large x) it is read from global memory half a chunk ahead and its pairs are picked at each use.
@@ -491,7 +502,7 @@ struct GemvKernel {
     float tot[MT][NT][4], acc[MT][NT][4];
 
     // x of kAhead blocks of the chunk at entry k, as it stands in memory, read one such part ahead
-    constexpr int kAhead = NT == 1 ? 4 : 2, kParts = kChunk / 32 / kAhead;
+    constexpr int kAhead = 4, kParts = kChunk / 32 / kAhead;
     const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
     // Where the first group of this lane's row of tile i stands within a piece, in bytes; a further stage
     // moves that on unless its groups fill pieces.
@@ -690,23 +701,27 @@ int by_group(const GemvW4& p, cudaStream_t s) {
   return launch_gemv<XT, NT, MT, S, WK, SWIGLU, XW, false, 1>(p, s);
 }
 
-// x as a whole in shared memory where it fits beside the ring, and is one tile's rows of one matrix.
+// x as a whole in shared memory where it fits beside the ring, and is one tile's rows of one matrix
+// (one and eight rows through [151936, 4096]: 62 and 64 us, against 69 and 79 us read from global memory;
+// through [5120, 5120]: 7.0 and 8.1 against 9.5 and 10.5 us).
 template <int XT, int NT, int MT, int S, int WK, bool SWIGLU>
 bool x_fits(const GemvW4& p) {
   using Kern = GemvKernel<XT, NT, MT, S, WK, SWIGLU, true, true, 1>;  // the largest stages
   return !p.offsets && p.M <= Kern::kTok && p.M * (int64_t)Kern::x_stride((int)p.K) <= kSmemMax - Kern::kFixed;
 }
 
+// A K of no more than two chunks leaves two of four warps along K without work: those go along the
+// columns instead ([160000, 512]: 15 against 27 us).  Nine to sixteen rows share a tile where their x
+// fits shared memory (12 rows through [16384, 2048]: 8.5 us, against 12.3 us as two tiles); where it does
+// not, two tiles of eight are faster (16 rows through [75000, 4096]: 82 against 89 us).
 template <int XT>
 int gemv_w4_plain(const GemvW4& p, cudaStream_t s) {
   if (p.K <= 2 * kChunk)
     return x_fits<XT, 1, 1, 3, 2, false>(p) ? by_group<XT, 1, 1, 3, 2, false, true>(p, s)
                                             : by_group<XT, 1, 2, 2, 2, false, false>(p, s);
   if (x_fits<XT, 1, 1, 3, 4, false>(p)) return by_group<XT, 1, 1, 3, 4, false, true>(p, s);
-  // sixteen rows of x per tile only where eight would leave a second tile per matrix
-  if (p.M <= 8 * p.E) return by_group<XT, 1, 2, 2, 4, false, false>(p, s);
   return x_fits<XT, 2, 1, 2, 4, false>(p) ? by_group<XT, 2, 1, 2, 4, false, true>(p, s)
-                                          : by_group<XT, 2, 1, 3, 4, false, false>(p, s);
+                                          : by_group<XT, 1, 2, 2, 4, false, false>(p, s);
 }
 
 template <int XT>

@@ -319,7 +319,8 @@ struct GemvKernel {
   static constexpr int kTableAt = 256, kBarriers = 1024;
   static_assert(kTeams * S * 16 <= kTableAt && kTableAt + 4 * kBlocks <= kBarriers);
   static constexpr int kRing = kBarriers + 2 * kMulWarps * kPartial * 4;
-  static constexpr int kFixed = kRing + kTeams * S * kStage;
+  // then 512 zero bytes, at the banks that an odd row of x has, and x
+  static constexpr int kZeroX = kRing + kTeams * S * kStage + 64, kFixed = kZeroX + 2 * kChunk + 64;
 
   static __host__ __device__ __forceinline__ int x_stride(int K) {
     return (2 * K + 127) / 128 * 128 + 64;  // two neighbouring rows of x never meet in a bank
@@ -476,6 +477,7 @@ struct GemvKernel {
     float* const partials = reinterpret_cast<float*>(smem + kBarriers);  // [buffer][warp][tile][token][row]
     uint8_t* const x_all = smem + kFixed;
     if (XW) {
+      if (threadIdx.x < 2 * kChunk / 16) reinterpret_cast<uint4*>(smem + kZeroX)[threadIdx.x] = make_uint4(0, 0, 0, 0);
       const int pieces = K / 8;
       for (int j = threadIdx.x; j < pieces; j += 32 * kMulWarps) {
         uint4 v[kTok];  // every row's loads in flight together
@@ -503,7 +505,8 @@ struct GemvKernel {
 
     // x of kAhead blocks of the chunk at entry k, as it stands in memory, read one such part ahead
     constexpr int kAhead = 4, kParts = kChunk / 32 / kAhead;
-    const uint8_t* x_row[NT];  // this lane's rows of x (columns past the last row are not stored)
+    const uint8_t* x_row[NT];  // this lane's rows of x; columns past the last row are 0 (and not stored):
+    int x_on[NT];              // the MMA draws less power so, and power is what limits the clock
     // Where the first group of this lane's row of tile i stands within a piece, in bytes; a further stage
     // moves that on unless its groups fill pieces.
     int scale_odd[MT], zero_odd[MT];
@@ -541,7 +544,7 @@ struct GemvKernel {
           for (int n = 0; n < NT; ++n) {
             uint4 b;
             if constexpr (XW) {
-              b = *reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * jj);
+              b = *reinterpret_cast<const uint4*>(x_row[n] + (2 * k & x_on[n]) + 64 * jj);
             } else {
               b = xv[n][jj % kAhead];
               b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
@@ -591,9 +594,12 @@ struct GemvKernel {
       const int rows = walk.rows();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int m = min(8 * n + g, rows - 1);
-        x_row[n] = XW ? x_all + m * x_stride(K) + 16 * t
-                      : reinterpret_cast<const uint8_t*>(p.x) + ((walk.tok.m0 + m) * K + 8 * t) * 2;
+        const int m = 8 * n + g;
+        x_on[n] = m < rows ? -1 : 0;
+        if (XW)
+          x_row[n] = (m < rows ? x_all + m * x_stride(K) : smem + kZeroX) + 16 * t;
+        else
+          x_row[n] = reinterpret_cast<const uint8_t*>(p.x) + ((walk.tok.m0 + min(m, rows - 1)) * K + 8 * t) * 2;
       }
       for (int k = kw * kChunk; k < K + kw * kChunk; k += kStep) {  // every warp meets every stage
         const int blocks = min(kChunk / 32, (K - k) / 32);

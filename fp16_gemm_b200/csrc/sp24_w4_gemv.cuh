@@ -281,15 +281,17 @@ struct Walk {
 // they come, with x's pairs picked alike.  A group's sum is scaled in fp32.
 //
 // What bounds it: the bytes of codes and scales for large matrices (one token through [151936, 4096],
-// groups of 128: 62 us, 5.2 TB/s, 0.79 of the copy rate), with instruction issue close behind: a chunk of 16
-// rows, 2 KB, takes about 190 instructions of products proper, and an SM has 88 cycles for it at that
-// rate.  Hence warps of their own for the copies (68 against 74 us with every warp copying for itself:
-// no registers are left for its addresses), chunks of 256 instead of 128 entries, expand8 (74 against
-// 80 us with the codes or-ed into 2^7 and a subtraction), and tables copied per stage of four chunks
-// (groups of 32 with zero points: 86 against 146 us with a row's few bytes copied per chunk).  Small
-// matrices are bound by the launch, the first loads and a warp's own latency through its few chunks
-// ([5120, 5120]: 7 us, floor 2.1).  Experts (8 tokens over 10 of 512, SwiGLU, [1024, 2048] each: 25 us, 3.3 TB/s)
-// spend half of their instructions between items of two chunks a warp.
+// groups of 128: 61 us, 5.2 TB/s, 0.80 of the copy rate; 68 us under sustained load, where the power
+// limit takes the clock from 1965 to 1770 MHz), with instruction issue close behind: a chunk of 16
+// rows, 2 KB, takes about 190 instructions of products proper, and an SM has 88 cycles for it at
+// the copy rate.  Hence warps of their own for the copies (68 against 74 us with every warp copying
+// for itself: no registers are left for its addresses), chunks of 256 instead of 128 entries, expand8
+// (74 against 80 us with the codes or-ed into 2^7 and a subtraction), and tables copied per stage of
+// four chunks (groups of 32 with zero points: 86 against 146 us with a row's few bytes copied per
+// chunk).  Small matrices are bound by the launch, the first loads and a warp's own latency through
+// its few chunks ([5120, 5120]: 7 us, floor 2.1).  Experts (8 tokens over 10 of 512, SwiGLU,
+// [1024, 2048] each: 25 us, 3.3 TB/s) spend half of their instructions between items of two chunks a
+// warp.
 //
 // XW: x stands in shared memory whole, its pairs picked when it is brought there; otherwise (experts,
 // or a large x) it is read from global memory half a chunk ahead and its pairs are picked at each use.

@@ -6,7 +6,7 @@
 // 4096 tokens x 10 slots, rows of 2048 bf16 entries (185 MB moved one way, 28 us at the copy rate): sort 34 us,
 // its gradient 27 us, unsort 28 us, its gradients 57 us (354 MB, 54 us).  A decode step (8 tokens): about 3 us
 // each, the time of a launch and two dependent loads.
-#include "sp24_internal.cuh"
+#include "sp24_launch.cuh"
 
 namespace sp24 {
 namespace {
@@ -170,27 +170,6 @@ __device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t
   copy_batches<BYTES, 1>(to, from, vecs, c);
 }
 
-// Programmatic dependent launch: a kernel lets the next one of its stream start early, and that one
-// waits (in hardware) for its predecessor's end before it touches what that writes.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... P, typename... A>
-int launch_after(void (*kernel)(P...), unsigned ctas, unsigned threads, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-  count_launch(1);
-  return e == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
-}
-
 // One warp per entry, then one per offset.
 template <int BYTES>
 __global__ void __launch_bounds__(32 * kWarps) sort_few_kernel(const __grid_constant__ SortTables t,
@@ -198,6 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps) sort_few_kernel(const __grid_cons
                                                                int64_t row_bytes, uint8_t* __restrict__ xs) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * kWarps + (threadIdx.x >> 5), n = (int)t.n;
+  begin();
   if (i >= n + t.E + 1) return;
   const int32_t id = i < n ? t.routing[i] : i - n;
   const int key = entry_key(id, t.E);
@@ -224,7 +204,7 @@ __global__ void __launch_bounds__(256) sort_count_kernel(const int32_t* __restri
                                                          int chunk_log, int64_t chunks, int32_t* __restrict__ counts,
                                                          int32_t* __restrict__ done) {
   extern __shared__ int32_t held[];
-  let_next_start();
+  begin();
   if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
   const int64_t from = (int64_t)blockIdx.x << chunk_log, to = min(n, from + ((int64_t)1 << chunk_log));
   for (int e0 = 0; e0 <= E; e0 += kCounters) {
@@ -261,8 +241,7 @@ __global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restr
                                                                 int32_t* __restrict__ done) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t e = (int64_t)blockIdx.x * kWarps + warp;
-  let_next_start();
-  wait_for_previous();
+  begin();
   if (e <= E) {
     int32_t* const mine = counts + e * chunks;
     int carry = 0;
@@ -317,6 +296,7 @@ __global__ void __launch_bounds__(kParts * kEntries) sort_many_kernel(const __gr
   __shared__ int rows[kEntries];
   const int64_t i0 = (int64_t)blockIdx.x * kEntries, from = i0 >> t.chunk_log << t.chunk_log;
   const int mine = (int)min((int64_t)kEntries, t.n - i0), ahead = (int)(i0 - from);
+  // the keys are read before the wait: the kernel before this one, the scan, does not write them
   for (int j = threadIdx.x; j < ahead + mine; j += kParts * kEntries) {
     const int32_t id = t.routing[from + j];
     const int key = entry_key(id, t.E);
@@ -331,7 +311,7 @@ __global__ void __launch_bounds__(kParts * kEntries) sort_many_kernel(const __gr
     for (int j = part; j < ahead + i; j += kParts) equal += keys[j] == key;
 #pragma unroll
   for (int d = 1; d < kParts; d <<= 1) equal += __shfl_xor_sync(kFull, equal, d);
-  wait_for_previous();
+  begin();
   if (i < mine && part == 0) {
     const int row = t.first[key] + t.before[key * t.chunks + (i0 >> t.chunk_log)] + equal;
     put_entry(t, i0 + i, key, row);
@@ -387,6 +367,7 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restr
   constexpr int kIn = V * Elem<YS>::kBytes, kOut = V * Elem<Y>::kBytes;
   const int lane = threadIdx.x & 31;
   const uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  begin();
   if (u >= units) return;
   const uint32_t t = u / per_row;
   const int64_t c = (int64_t)(u - t * per_row) * (32 * W) + lane;
@@ -441,6 +422,7 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_backward_kernel(
   constexpr int kIn = V * Elem<YS>::kBytes, kOut = V * Elem<Y>::kBytes;
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  begin();
   if (i >= n) return;
   const int r = entry_row(pos, i, rows);
   if (r < 0) {
@@ -560,11 +542,10 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
     int32_t* const first = reinterpret_cast<int32_t*>(base + ws.first_at);
     int32_t* const before = reinterpret_cast<int32_t*>(base + ws.before_at);
     const int64_t counters = E + 1 < kCounters ? E + 1 : kCounters;
-    sort_count_kernel<<<(unsigned)ws.chunks, 256, (size_t)counters * 4, s>>>(routing, n, E, ws.chunk_log, ws.chunks,
-                                                                             before, done);
-    st = launch_status();
+    st = launch_after(sort_count_kernel, (unsigned)ws.chunks, 256, (size_t)counters * 4, s, routing, n, E, ws.chunk_log,
+                      ws.chunks, before, done);
     if (st) return st;
-    st = launch_after(sort_scan_kernel, (unsigned)((E + kWarps) / kWarps), 32 * kWarps, s, before, E, ws.chunks, first,
+    st = launch_after(sort_scan_kernel, (unsigned)((E + kWarps) / kWarps), 32 * kWarps, 0, s, before, E, ws.chunks, first,
                       offsets, done);
     if (st) return st;
     t.first = first;
@@ -576,10 +557,10 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   auto run = [&](auto bytes) {
     constexpr int B = decltype(bytes)::value;
     if (ws.bytes)
-      return launch_after(sort_many_kernel<B>, (unsigned)((n + kEntries - 1) / kEntries), kParts * kEntries, s, t, from,
-                          topk, row, to);
-    sort_few_kernel<B><<<(unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s>>>(t, from, topk, row, to);
-    return launch_status();
+      return launch_after(sort_many_kernel<B>, (unsigned)((n + kEntries - 1) / kEntries), kParts * kEntries, 0, s, t,
+                          from, topk, row, to);
+    return launch_after(sort_few_kernel<B>, (unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s, t, from, topk, row,
+                        to);
   };
   if (row % 16 == 0 && aligned(x, 16) && aligned(xs, 16)) return run(std::integral_constant<int, 16>{});
   if (row % 4 == 0 && aligned(x, 4) && aligned(xs, 4)) return run(std::integral_constant<int, 4>{});
@@ -603,10 +584,9 @@ extern "C" int sp24_moe_unsort(const void* ys, int ys_dtype, const int32_t* pos,
         constexpr int W = decltype(wide)::value, S = decltype(slots)::value;
         const int64_t per_row = (H / V + 32 * W - 1) / (32 * W), units = T * per_row;
         if (units > INT32_MAX) return (int)SP24_ERR_UNSUPPORTED;  // more than any device's memory holds
-        unsort_kernel<decltype(p)::ys, decltype(p)::y, V, W, S>
-            <<<(unsigned)((units + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(
-                ys, pos, router_w, (uint32_t)units, (uint32_t)per_row, topk, rows, H / V, y);
-        return launch_status();
+        return launch_after(unsort_kernel<decltype(p)::ys, decltype(p)::y, V, W, S>,
+                            (unsigned)((units + kWarps - 1) / kWarps), 32 * kWarps, 0, s, ys, pos, router_w,
+                            (uint32_t)units, (uint32_t)per_row, topk, rows, H / V, y);
       };
       constexpr int W = V >= 4 ? 2 : 8 / V;
       if (topk <= 2) return go(std::integral_constant<int, W>{}, std::integral_constant<int, 2>{});
@@ -638,12 +618,10 @@ extern "C" int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void*
       constexpr int V = decltype(vec)::value;
       const unsigned ctas = (unsigned)((n + kWarps - 1) / kWarps);
       if (d_router_w)
-        unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, true>
-            <<<ctas, 32 * kWarps, 0, s>>>(dy, ys, pos, router_w, n, topk, rows, H / V, dys, d_router_w);
-      else
-        unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, false>
-            <<<ctas, 32 * kWarps, 0, s>>>(dy, ys, pos, router_w, n, topk, rows, H / V, dys, nullptr);
-      return launch_status();
+        return launch_after(unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, true>, ctas, 32 * kWarps, 0, s, dy, ys,
+                            pos, router_w, n, topk, rows, H / V, dys, d_router_w);
+      return launch_after(unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, false>, ctas, 32 * kWarps, 0, s, dy, ys,
+                          pos, router_w, n, topk, rows, H / V, dys, nullptr);
     };
     if (v == 8) return run(std::integral_constant<int, 8>{});
     if (v == 4) return run(std::integral_constant<int, 4>{});

@@ -1,6 +1,7 @@
 // 4-bit integer weights with one scale (and zero point) per group of 32, 64 or 128 entries of a
 // row: quantiser, dequantiser, and the products of a few rows with such weights (definitions in
 // sp24.h).
+#include "sp24_launch.cuh"
 #include "sp24_w4.cuh"
 
 namespace sp24 {
@@ -54,6 +55,7 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* __restric
   using P = typename Pair16<DT>::T;
   const int lane = threadIdx.x % L;
   const int64_t step = (int64_t)gridDim.x * (256 / L);
+  begin();
   // every lane of a group is in range together; those of other groups in the warp may not be
   for (int64_t group = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; group < (groups + 31) / 32 * 32; group += step) {
     const bool live = group < groups;
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __re
                                                             const uint8_t* __restrict__ zeros, int64_t vecs,
                                                             int span_log, void* __restrict__ out) {
   constexpr int kTurns = 4;
+  begin();
   for (int64_t base = (int64_t)blockIdx.x * (256 * kTurns) + threadIdx.x; base < vecs;
        base += (int64_t)gridDim.x * (256 * kTurns)) {
     uint32_t c[kTurns], s16[kTurns], z[kTurns];
@@ -222,15 +225,9 @@ template <int DT, int G>
 int quantize(const void* w, int64_t groups, bool with_zeros, uint8_t* codes, void* scales, uint8_t* zeros,
              cudaStream_t s) {
   const unsigned ctas = stream_ctas((groups * (G / 16) + 255) / 256);
-  if (with_zeros)
-    quantize_w4_kernel<DT, G, true><<<ctas, 256, 0, s>>>(reinterpret_cast<const uint4*>(w), groups,
-                                                         reinterpret_cast<uint32_t*>(codes),
-                                                         reinterpret_cast<uint16_t*>(scales), zeros);
-  else
-    quantize_w4_kernel<DT, G, false><<<ctas, 256, 0, s>>>(reinterpret_cast<const uint4*>(w), groups,
-                                                          reinterpret_cast<uint32_t*>(codes),
-                                                          reinterpret_cast<uint16_t*>(scales), nullptr);
-  return launch_status();
+  return launch_after(with_zeros ? quantize_w4_kernel<DT, G, true> : quantize_w4_kernel<DT, G, false>, ctas, 256, 0, s,
+                      reinterpret_cast<const uint4*>(w), groups, reinterpret_cast<uint32_t*>(codes),
+                      reinterpret_cast<uint16_t*>(scales), zeros);
 }
 
 template <int DT>
@@ -247,11 +244,8 @@ int dequantize(const sp24_w4_operand* w, int64_t vecs, void* out, cudaStream_t s
   const uint32_t* c = reinterpret_cast<const uint32_t*>(w->codes);
   const uint16_t* sc = reinterpret_cast<const uint16_t*>(w->scales);
   const int span_log = w->group == 128 ? 4 : w->group == 64 ? 3 : 2;
-  if (w->scale_dtype == SP24_BF16)
-    dequantize_w4_kernel<DT, SP24_BF16><<<ctas, 256, 0, s>>>(c, sc, w->zeros, vecs, span_log, out);
-  else
-    dequantize_w4_kernel<DT, SP24_F16><<<ctas, 256, 0, s>>>(c, sc, w->zeros, vecs, span_log, out);
-  return launch_status();
+  return launch_after(w->scale_dtype == SP24_BF16 ? dequantize_w4_kernel<DT, SP24_BF16> : dequantize_w4_kernel<DT, SP24_F16>,
+                      ctas, 256, 0, s, c, sc, w->zeros, vecs, span_log, out);
 }
 
 }  // namespace

@@ -1,6 +1,7 @@
 // The kernel of sp24_gemv_w4 / sp24_gemv_w4_grouped; each type of x is a translation unit of its own.
 #pragma once
 
+#include "sp24_launch.cuh"
 #include "sp24_tc.cuh"
 #include "sp24_w4.cuh"
 
@@ -341,6 +342,7 @@ struct GemvKernel {
       tc::fence_mbar_init();
     }
     int* const table = reinterpret_cast<int*>(smem + kTableAt);
+    begin();
     if (p.offsets)
       for (int b = warp; b < min((int)((p.E + 31) / 32), kBlocks); b += kMulWarps + kTeams) table[b] = block_tiles<kTok>(p, b);
     __syncthreads();
@@ -693,8 +695,7 @@ int launch_gemv(const GemvW4& p, cudaStream_t s) {
   if (items > INT32_MAX / 2) return SP24_ERR_UNSUPPORTED;
   const int sms = sm_count();
   const int64_t ctas = items < sms ? items : sms;
-  kernel<<<(unsigned)ctas, 32 * (kMulWarps + kTeams), (size_t)Kern::smem_bytes(p), s>>>(p);
-  return launch_status();
+  return launch_after(kernel, (unsigned)ctas, 32 * (kMulWarps + kTeams), (size_t)Kern::smem_bytes(p), s, p);
 }
 
 template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW>

@@ -480,6 +480,36 @@ def test_sorts_at_once_on_two_streams():
     assert all(torch.equal(a, b) for i, t in got for a, b in zip(t[1:], want[i][1:]))
 
 
+@pytest.mark.parametrize("T", [100, 1500, 12000])
+def test_calls_without_a_wait_between(T):
+    """Each call starts while the one before it ends: what it reads has to be written all the same."""
+    g = torch.Generator().manual_seed(T)
+    E, k, H = 64, 4, 64
+    logits = [torch.randn(T, E, generator=g).cuda() for _ in range(4)]
+    x = torch.randn(T, H, generator=g).cuda()
+
+    def step(l, wait):
+        routing, w = sp.moe_route(l, k)
+        if wait:
+            torch.cuda.synchronize()
+        s = sp.moe_sort(x, routing, E)
+        if wait:
+            torch.cuda.synchronize()
+        y = sp.moe_unsort(s.xs, s.pos, w)
+        if wait:
+            torch.cuda.synchronize()
+        dys, dw = sp.moe_unsort_backward(y, s.xs, s.pos, w)
+        if wait:
+            torch.cuda.synchronize()
+        return [routing, *s, y, dys, dw, sp.moe_route_backward(dw, l, routing)]
+
+    want = [step(l, True) for l in logits]
+    got = [step(logits[i % 4], False) for i in range(24)]
+    _cuda_ok()
+    for i, r in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i % 4]))
+
+
 def test_route_weights_of_one_expert_and_extremes():
     """One expert; logits at the type's ends (differences that overflow to infinity included)."""
     l = torch.tensor([[3.0e38, -3.0e38, 1.0, 3.0e38], [-3.0e38, -3.0e38, -3.0e38, -3.0e38]], device="cuda")

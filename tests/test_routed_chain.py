@@ -50,6 +50,35 @@ def test_decode_step(dtype, T, E, k, H, F):
     assert T <= 2 or (out[-1] == 0).all()
 
 
+def test_decode_steps_without_a_wait_between():
+    """The step repeated on new tokens with nothing waited for in between, weights quantised on the way."""
+    T, E, k, H, F = 8, 32, 6, 256, 96
+    g = torch.Generator().manual_seed(1)
+    xs = [torch.randn(T, H, generator=g).bfloat16().cuda() for _ in range(3)]
+    ls = [torch.randn(T, E, generator=g).cuda() for _ in range(3)]
+    wg = (torch.randn(E * 2 * F, H, generator=g) * 0.05).bfloat16().cuda()
+    wd = (torch.randn(E * H, F, generator=g) * 0.05).bfloat16().cuda()
+
+    def step(x, l, done):
+        gu, dn = sp.quantize_w4(wg, 64, True), sp.quantize_w4(wd, 32)
+        done()
+        routing, w = sp.moe_route(l, k)
+        done()
+        s = sp.moe_sort(x, routing, E)
+        done()
+        h = sp.gemv_w4_grouped(s.xs, gu, s.offsets, sp.ACT_SWIGLU)
+        done()
+        y = sp.gemv_w4_grouped(h, dn, s.offsets)
+        done()
+        return sp.moe_unsort(y, s.pos, w), sp.dequantize_w4(dn)
+
+    want = [step(x, l, torch.cuda.synchronize) for x, l in zip(xs, ls)]
+    got = [step(xs[i % 3], ls[i % 3], lambda: None) for i in range(18)]
+    torch.cuda.synchronize()
+    assert sp.last_device_error() == sp.OK
+    assert all(torch.equal(a, b) for i, r in enumerate(got) for a, b in zip(r, want[i % 3]))
+
+
 @pytest.mark.parametrize("form", [(sp.ROUTE_SOFTMAX, True), (sp.ROUTE_SOFTMAX, False), (sp.ROUTE_SIGMOID, True)],
                          ids=["softmax_renorm", "softmax", "sigmoid_renorm"])
 def test_training_step(form):

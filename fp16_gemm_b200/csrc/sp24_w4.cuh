@@ -28,6 +28,7 @@ struct GemvW4 {
   void* y;
   int64_t M, E, N, K;
   int scale_dtype, group, y_f32;
+  int share;  // set by the launch: the teams of a CTA that take an item's K together, all or one
 };
 
 int gemv_w4_bf16(const GemvW4& p, cudaStream_t s);

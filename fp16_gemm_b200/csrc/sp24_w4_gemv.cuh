@@ -275,7 +275,8 @@ struct Walk {
 // multiply, each a chunk of every four; mbarriers tell the stages full and empty.  The four chunks
 // follow each other along K (WK 4), or, where K has no more than two, pairs of them along the columns
 // (WK 2).  The partial sums of the warps that share K meet in shared memory in a fixed order, in two
-// buffers that take turns, so one barrier of the team per item is enough.
+// buffers that take turns, so one barrier of the team per item is enough.  Where there are few items, the
+// four teams take every fourth step of one item's K, and that barrier is the CTA's.
 //
 // An ldmatrix of 16-byte row pieces hands lane (g, t) the eight codes 8t .. 8t + 7 of a 32-entry block
 // of rows g and g + 8; the MMA may sum K in any order, so the pairs that expand8 gives are fed as
@@ -348,12 +349,15 @@ struct GemvKernel {
     __syncthreads();
     const bool copies = warp >= kMulWarps;
     const int in_cta = copies ? warp - kMulWarps : warp / kMulPerTeam;
-    const int team = in_cta * gridDim.x + blockIdx.x, teams = gridDim.x * kTeams;
+    // teams that share an item walk the same items and take every kTeams-th step of K
+    const bool alone = p.share == 1;
+    const int team = (alone ? in_cta * gridDim.x : 0) + blockIdx.x, teams = alone ? gridDim.x * kTeams : gridDim.x;
+    const int k_first = alone ? 0 : in_cta * kStep, k_step = p.share * kStep;
     uint8_t* const ring = smem + kRing + in_cta * (S * kStage);
     if (copies)
-      copy(p, table, ring, bars + 2 * S * in_cta, team, teams);
+      copy(p, table, ring, bars + 2 * S * in_cta, team, teams, k_first, k_step);
     else
-      multiply_all(p, smem, ring, bars + 2 * S * in_cta, warp, in_cta, team, teams);
+      multiply_all(p, smem, ring, bars + 2 * S * in_cta, warp, in_cta, team, teams, k_first, k_step);
   }
 
   static __device__ __forceinline__ int64_t columns(const GemvW4& p) { return SWIGLU ? p.N / 2 : p.N; }
@@ -362,7 +366,8 @@ struct GemvKernel {
   }
 
   // ---- the copying warp: lane l copies piece l & 7 of rows (l >> 3) + 4 h of each of the four chunks
-  static __device__ __forceinline__ void copy(const GemvW4& p, const int* table, uint8_t* ring, uint64_t* bars, int team, int teams) {
+  static __device__ __forceinline__ void copy(const GemvW4& p, const int* table, uint8_t* ring, uint64_t* bars, int team,
+                                              int teams, int k_first, int k_step) {
     const int lane = threadIdx.x & 31;
     const int64_t cols = columns(p);
     const int col_tiles = column_tiles(p);
@@ -392,13 +397,14 @@ struct GemvKernel {
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int h = 0; h < 4; ++h)
-          code_src[i][h] = p.codes + (row0 + (SWIGLU ? i * cols : 16 * i) + (lane >> 3) + 4 * h) * (K / 2) + 16 * (lane & 7);
+          code_src[i][h] =
+              p.codes + (row0 + (SWIGLU ? i * cols : 16 * i) + (lane >> 3) + 4 * h) * (K / 2) + 16 * (lane & 7) + k_first / 2;
       // the first group of table row r's weight row: of the item's first row, and from there on
       const int64_t base0 = row0 * KG, base1 = SWIGLU ? (row0 + cols) * KG : base0;
       auto base = [&](int r) { return SWIGLU && (r & 16) ? base1 : base0; };
       auto row_of = [&](int r) { return SWIGLU ? (r & 15) + (r >> 5) * 16 : r; };  // within the item
 
-      for (int k0 = 0; k0 < K; k0 += kStep) {
+      for (int k0 = k_first; k0 < K; k0 += k_step) {
         if (round && !tc::mbar_wait(bars + 2 * stage + 1, (round - 1) & 1)) {
           set_dev_error(SP24_ERR_DEVICE_TIMEOUT);
           copy_wait_all();
@@ -463,7 +469,7 @@ struct GemvKernel {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) code_src[i][h] += kStep / 2;
+          for (int h = 0; h < 4; ++h) code_src[i][h] += k_step / 2;
         if (++stage == S) stage = 0, ++round;
       }
     }
@@ -472,7 +478,7 @@ struct GemvKernel {
 
   // ---- a multiplying warp
   static __device__ __forceinline__ void multiply_all(const GemvW4& p, uint8_t* smem, uint8_t* ring, uint64_t* bars,
-                                                      int warp, int in_cta, int team, int teams) {
+                                                      int warp, int in_cta, int team, int teams, int k_first, int k_step) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int in_team = warp & (kMulPerTeam - 1), kw = in_team % WK, sub = in_team / WK;
     const int64_t cols = columns(p);
@@ -605,7 +611,7 @@ struct GemvKernel {
         else
           x_row[n] = reinterpret_cast<const uint8_t*>(p.x) + ((walk.tok.m0 + min(m, rows - 1)) * K + 8 * t) * 2;
       }
-      for (int k = kw * kChunk; k < K + kw * kChunk; k += kStep) {  // every warp meets every stage
+      for (int k = k_first + kw * kChunk; k < K + kw * kChunk; k += k_step) {  // every warp meets every stage
         const int blocks = min(kChunk / 32, (K - k) / 32);
         const uint32_t at = stage * kStage;
         uint4 x[2][NT][kAhead];
@@ -643,21 +649,30 @@ struct GemvKernel {
             const int m = 8 * n + 2 * t + (k & 1);
             if (m < rows) mine[(i * kTok + m) * 16 + g + 8 * (k >> 1)] = tot[i][n][k] * (1.0f / Expand<XT>::kUnit);
           }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + in_cta), "r"(32 * kMulPerTeam) : "memory");
-      const float* const sums = partials + (buffer * kMulWarps + in_cta * kMulPerTeam) * kPartial;
+      const bool alone = p.share == 1;
+      if (alone)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + in_cta), "r"(32 * kMulPerTeam) : "memory");
+      else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + kTeams), "r"(32 * kMulWarps) : "memory");
+      const float* const sums = partials + (buffer * kMulWarps + (alone ? in_cta * kMulPerTeam : 0)) * kPartial;
       constexpr int kOutTiles = SWIGLU ? 1 : MT;
       constexpr int kTiles = kItemCols / 16;
-      for (int o = in_team * 32 + lane; o < rows * kTiles * 16; o += 32 * kMulPerTeam) {
+      for (int o = (alone ? in_team : warp) * 32 + lane; o < rows * kTiles * 16; o += p.share * 32 * kMulPerTeam) {
         const int r = o & 15, tile = (o >> 4) % kTiles, m = (o >> 4) / kTiles;
         const int64_t col = (int64_t)walk.col * kItemCols + 16 * tile + r;
         if (col >= cols) continue;
         const int i = tile % kOutTiles, first = tile / kOutTiles * WK;
         float v = 0.0f, up = 0.0f;
+        auto add = [&](const float* from) {
 #pragma unroll
-        for (int k = first; k < first + WK; ++k) {
-          v += sums[k * kPartial + (i * kTok + m) * 16 + r];
-          if (SWIGLU) up += sums[k * kPartial + (kTok + m) * 16 + r];
-        }
+          for (int k = 0; k < WK; ++k) {
+            v += from[k * kPartial + (i * kTok + m) * 16 + r];
+            if (SWIGLU) up += from[k * kPartial + (kTok + m) * 16 + r];
+          }
+        };
+        add(sums + first * kPartial);
+        if (!alone)
+          for (int q = 1; q < kTeams; ++q) add(sums + (q * kMulPerTeam + first) * kPartial);
         if (SWIGLU) v = v / (1.0f + expf(-v)) * up;
         const int64_t out = (walk.tok.m0 + m) * cols + col;
         if (p.y_f32)
@@ -677,7 +692,7 @@ __global__ void __launch_bounds__(32 * (kMulWarps + kTeams), 1) gemv_w4_kernel(c
 }
 
 template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW, bool ZEROS, int GB>
-int launch_gemv(const GemvW4& p, cudaStream_t s) {
+int launch_gemv(GemvW4 p, cudaStream_t s) {
   using Kern = GemvKernel<XT, NT, MT, S, WK, SWIGLU, XW, ZEROS, GB>;
   auto kernel = gemv_w4_kernel<XT, NT, MT, S, WK, SWIGLU, XW, ZEROS, GB>;
   static bool raised[64];  // the attribute holds per device
@@ -693,7 +708,14 @@ int launch_gemv(const GemvW4& p, cudaStream_t s) {
   const int64_t tok_tiles = (p.M + Kern::kTok - 1) / Kern::kTok + (p.offsets ? (p.E < p.M ? p.E : p.M) : 0);
   const int64_t items = col_tiles * tok_tiles;
   if (items > INT32_MAX / 2) return SP24_ERR_UNSUPPORTED;
+  // Few items: the four teams of a CTA take the K of one together.  The cost is rounds of items times
+  // steps of K and about one for an item's ends (12 rows through [48, 11232], groups of 32 with zero
+  // points: 15 us shared, 23 alone).
   const int sms = sm_count();
+  const int64_t steps = (p.K + Kern::kStep - 1) / Kern::kStep;
+  const int64_t alone = (items + kTeams * sms - 1) / (kTeams * sms) * (steps + 1);
+  const int64_t shared = (items + sms - 1) / sms * ((steps + kTeams - 1) / kTeams + 1);
+  p.share = shared < alone ? kTeams : 1;
   const int64_t ctas = items < sms ? items : sms;
   return launch_after(kernel, (unsigned)ctas, 32 * (kMulWarps + kTeams), (size_t)Kern::smem_bytes(p), s, p);
 }
@@ -720,7 +742,8 @@ bool x_fits(const GemvW4& p) {
 }
 
 // A K of no more than two chunks leaves two of four warps along K without work: those go along the
-// columns instead ([160000, 512]: 15 against 27 us).  Nine to sixteen rows share a tile where their x
+// columns instead ([160000, 512]: 15 against 27 us).  A third stage is worth 2 % (64 against 65.5 us above)
+// and given up for an x that then fits (4 rows of 16384: 8.8 against 14 us through [300, 16384]).  Nine to sixteen rows share a tile where their x
 // fits shared memory (12 rows through [16384, 2048]: 8.5 us, against 12.3 us as two tiles); where it does
 // not, two tiles of eight are faster (16 rows through [75000, 4096]: 82 against 89 us).
 template <int XT>
@@ -729,6 +752,7 @@ int gemv_w4_plain(const GemvW4& p, cudaStream_t s) {
     return x_fits<XT, 1, 1, 3, 2, false>(p) ? by_group<XT, 1, 1, 3, 2, false, true>(p, s)
                                             : by_group<XT, 1, 2, 2, 2, false, false>(p, s);
   if (x_fits<XT, 1, 1, 3, 4, false>(p)) return by_group<XT, 1, 1, 3, 4, false, true>(p, s);
+  if (x_fits<XT, 1, 1, 2, 4, false>(p)) return by_group<XT, 1, 1, 2, 4, false, true>(p, s);
   return x_fits<XT, 2, 1, 2, 4, false>(p) ? by_group<XT, 2, 1, 2, 4, false, true>(p, s)
                                           : by_group<XT, 1, 2, 2, 4, false, false>(p, s);
 }

@@ -214,7 +214,8 @@ def test_gemv_swiglu(M, F, K, G, dtype):
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("G", [32, 64, 128])
 @pytest.mark.parametrize("M,N,K", [(1, 70, 256), (3, 129, 384), (8, 33, 512), (11, 65, 512), (2, 47, 640), (8, 50, 16512),
-                                   (16, 37, 9088), (20, 48, 1152), (1, 2400, 1920)])
+                                   (16, 37, 9088), (20, 48, 1152), (1, 2400, 1920), (12, 48, 5248), (1, 2368, 3968), (1, 7000, 2560),
+                                   (4, 4800, 1152)])
 def test_gemv_paths(M, N, K, G, zeros):
     """One or two chunks of K, an x that does not fit shared memory, two tiles of rows, odd numbers of
     groups (rows of scales and zero points at every place within sixteen bytes)."""

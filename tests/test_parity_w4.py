@@ -228,6 +228,25 @@ def test_gemv_paths(M, N, K, G, zeros):
     _cuda_ok()
 
 
+def test_gemv_waits_that_run_out():
+    """With a wait limit that any wait outlasts, the call still ends, reports it at most, and the next
+    one is right."""
+    import ctypes
+    x = torch.randn(2, 4096, generator=_gen(1)).bfloat16().cuda()
+    w = random_w4(20000, 4096, 64, True, torch.bfloat16, 2)
+    want = sp.gemv_w4(x, w)
+    old = ctypes.c_ulonglong()
+    assert sp.lib().sp24_get_wait_limit(ctypes.byref(old)) == sp.OK
+    assert sp.lib().sp24_set_wait_limit(1) == sp.OK
+    try:
+        sp.gemv_w4(x, w)
+        assert sp.last_device_error() in (sp.OK, sp.ERR_DEVICE_TIMEOUT)
+    finally:
+        assert sp.lib().sp24_set_wait_limit(old.value) == sp.OK
+    assert torch.equal(sp.gemv_w4(x, w), want)
+    _cuda_ok()
+
+
 def test_gemv_two_streams_at_once():
     """Calls that overlap share nothing: the bits are those of calls made alone."""
     x = torch.randn(4, 2048, generator=_gen(1)).bfloat16().cuda()

@@ -1094,6 +1094,8 @@ def quantize_w4(w: torch.Tensor, group: int = 128, zeros: bool = False, out: Opt
         out = W4Tensor(torch.empty((R, K // 2), dtype=torch.uint8, device=dev),
                        torch.empty((R, K // group), dtype=w.dtype, device=dev),
                        torch.empty((R, K // group), dtype=torch.uint8, device=dev) if zeros else None)
+    elif (out.zeros is not None) != bool(zeros):
+        raise ValueError("out.zeros must be there exactly where zeros is asked for")
     zp = _arg(out.zeros, "zeros", dev, (R, K // group), torch.uint8) if zeros else None
     _check((_lib or lib()).sp24_quantize_w4(wp, _DT[w.dtype], R, K, group, bool(zeros),
                                   _arg(out.codes, "codes", dev, (R, K // 2), torch.uint8),
@@ -1107,6 +1109,8 @@ def dequantize_w4(w: W4Tensor, dtype=torch.float32, out=None) -> torch.Tensor:
     """The values (q - z) * s of 4-bit weights, rounded once to `dtype`."""
     dev = w.codes.get_device()
     op, rows, K = _w4(w, dev)
+    if dtype not in _FLOATS:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, not {dtype}")
     if out is None:
         out = torch.empty((rows, K), dtype=dtype, device=dev)
     _check((_lib or lib()).sp24_dequantize_w4(op, rows, K, _DT[dtype], _arg(out, "out", dev, (rows, K), dtype),

@@ -417,3 +417,54 @@ def test_refusals():
                       (lambda: sp.gemv_w4(x, sp.W4Tensor(w.codes.cpu(), w.scales)), ValueError)):
         with pytest.raises(err):
             call()
+
+
+def test_refusals_of_given_outputs_and_types():
+    w16 = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    plain, offset = sp.quantize_w4(w16, 64), sp.quantize_w4(w16, 64, True)
+    for call, err in ((lambda: sp.quantize_w4(w16, 64, False, out=offset), ValueError),
+                      (lambda: sp.quantize_w4(w16, 64, True, out=plain), ValueError),
+                      (lambda: sp.dequantize_w4(plain, torch.int32), TypeError),
+                      (lambda: sp.dequantize_w4(plain, torch.float64), TypeError),
+                      (lambda: sp.dequantize_w4(plain, out=w16), TypeError)):
+        with pytest.raises(err):
+            call()
+    _cuda_ok()
+
+
+def test_graph_of_branches_behind_copies():
+    """Captured launches that follow a fill or a copy, and ones that follow two joined branches."""
+    x = torch.randn(4, 512, generator=_gen(3)).bfloat16().cuda()
+    w16 = (torch.randn(96, 512, generator=_gen(4)) * 0.02).bfloat16().cuda()
+    held, staged = torch.empty_like(x), torch.empty_like(w16)
+    y, z = torch.empty(4, 96, device="cuda"), torch.empty(4, 96, device="cuda")
+    side = torch.cuda.Stream()
+
+    def chain():
+        y.zero_()
+        held.copy_(x)
+        staged.copy_(w16)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            a = sp.quantize_w4(staged, 64, True)
+            sp.gemv_w4(held, a, out=z)
+        b = sp.quantize_w4(staged, 32)
+        sp.gemv_w4(held, b, out=y)
+        torch.cuda.current_stream().wait_stream(side)
+        v, u = sp.dequantize_w4(a), sp.dequantize_w4(b)
+        return [y.clone(), z.clone(), v, u, sp.gemv_w4(held, a)]
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for seed in range(5, 9):
+        x.copy_(torch.randn(4, 512, generator=_gen(seed)))
+        w16.copy_(torch.randn(96, 512, generator=_gen(seed + 9)) * 0.02)
+        graph.replay()
+        graph.replay()
+        again = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(again, chain()))
+        torch.cuda.synchronize()
+    _cuda_ok()

@@ -3,9 +3,9 @@
 // sp24.h; [P1] "Concurrency, not sparsity, is the lever" names the routed model).
 //
 // Everything here moves rows; nothing is multiplied more than once, so HBM is the bound.  Measured at
-// 4096 tokens x 10 slots, rows of 2048 bf16 entries (185 MB moved one way, 28 us at the copy rate): sort 34 us,
-// its gradient 27 us, unsort 28 us, its gradients 57 us (354 MB, 54 us).  A decode step (8 tokens): about 3 us
-// each, the time of a launch and two dependent loads.
+// 4096 tokens x 10 slots, rows of 2048 bf16 entries (185 MB moved one way, 28 us at the copy rate): sort 36 us
+// (10 of them its tables), its gradient 27 us, unsort 27 us, its gradients 54 us (354 MB, 54 us).  A decode step (8
+// tokens): about 2.5 us each, the time of a launch and two dependent loads.
 #include "sp24_launch.cuh"
 
 namespace sp24 {
@@ -18,64 +18,37 @@ constexpr int kCounters = 8192;  // counters of one pass over a chunk (32 KB of 
 
 // ------------------------------------------------------------------ element access
 
-// V consecutive elements of type DT as 32-bit words (one half word for a single 16-bit element), moved
-// with accesses of at most 16 bytes, whatever the vector's size.
+// BYTES (4 to 32) consecutive bytes as 32-bit words, moved with accesses of at most 16 bytes.
 template <int BYTES>
 struct Words {
-  uint32_t w[BYTES < 4 ? 1 : BYTES / 4];
+  uint32_t w[BYTES / 4];
 };
 
 // Rows of tens of thousands of entries pass through L2 once: they are read and written with the
-// evict-first policy, which leaves the tokens' own rows (read topk times) there (sort 34 against 41 us,
-// unsort 28 against 33, its gradients 57 against 61).
-template <int BYTES>
-__device__ __forceinline__ Words<BYTES> load_stream(const void* base, int64_t index) {
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + index * BYTES;
-  Words<BYTES> r;
-  if constexpr (BYTES == 2) {
-    r.w[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
-  } else if constexpr (BYTES == 4) {
-    r.w[0] = __ldcs(reinterpret_cast<const unsigned int*>(p));
+// evict-first policy (STREAM), which leaves the tokens' own rows (read topk times) there (sort 34
+// against 41 us, unsort 28 against 33, its gradients 57 against 61).
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load_as(const uint8_t* p) {
+  return STREAM ? __ldcs(reinterpret_cast<const T*>(p)) : *reinterpret_cast<const T*>(p);
+}
+template <bool STREAM, int BYTES>
+__device__ __forceinline__ void load_vec(uint32_t* w, const uint8_t* p) {
+  if constexpr (BYTES == 4) {
+    w[0] = load_as<STREAM, unsigned int>(p);
   } else if constexpr (BYTES == 8) {
-    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
-    r.w[0] = v.x, r.w[1] = v.y;
+    const uint2 v = load_as<STREAM, uint2>(p);
+    w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+      const uint4 v = load_as<STREAM, uint4>(p + 16 * i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }
-  return r;
 }
-
 template <int BYTES>
-__device__ __forceinline__ Words<BYTES> load_words(const void* base, int64_t index) {
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + index * BYTES;
-  Words<BYTES> r;
-  if constexpr (BYTES == 2) {
-    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
-  } else if constexpr (BYTES == 4) {
-    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (BYTES == 8) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    r.w[0] = v.x, r.w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
-    }
-  }
-  return r;
-}
-
-template <int BYTES>
-__device__ __forceinline__ void store_stream(void* base, int64_t index, const Words<BYTES>& r) {
-  uint8_t* p = reinterpret_cast<uint8_t*>(base) + index * BYTES;
-  if constexpr (BYTES == 2) {
-    __stcs(reinterpret_cast<unsigned short*>(p), (unsigned short)r.w[0]);
-  } else if constexpr (BYTES == 4) {
+__device__ __forceinline__ void store_vec(uint8_t* p, const Words<BYTES>& r) {
+  if constexpr (BYTES == 4) {
     __stcs(reinterpret_cast<unsigned int*>(p), r.w[0]);
   } else if constexpr (BYTES == 8) {
     __stcs(reinterpret_cast<uint2*>(p), make_uint2(r.w[0], r.w[1]));
@@ -84,6 +57,103 @@ __device__ __forceinline__ void store_stream(void* base, int64_t index, const Wo
     for (int i = 0; i < BYTES / 16; ++i)
       __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]));
   }
+}
+
+// Rows of whole words (4, 8, 16 bytes) are moved by those.  Rows of 16-bit elements that start between
+// words ("ragged": odd widths, odd bases) are stored with aligned 16-byte vectors all the same, what is
+// ahead of the first and behind the last one by elements.  What a vector is made of is read as the
+// aligned 16-byte pieces around it and shifted, by the same amount all along a row.  4096 x 10 rows of
+// 2047 bf16 entries, against 2-byte accesses: sort 44 and 56 us, unsort 55 and 103, its gradients 84
+// and 110 (what is left are the shifts' instructions; where words do, they are faster: 2046 entries,
+// unsort 34 us).
+template <int BYTES, bool RAGGED>
+struct Window {
+  uint32_t w[BYTES / 4 + (RAGGED ? 4 : 0)];
+};
+
+// A row read by vectors of BYTES bytes, the first of which starts at p.
+template <int BYTES, bool RAGGED, bool STREAM>
+struct RowReader {
+  const uint8_t* at;
+  int shift;  // ragged: bytes between the aligned piece and the vector
+  __device__ __forceinline__ void start(const uint8_t* p) {
+    shift = RAGGED ? (int)((uintptr_t)p & 15) : 0;
+    at = p - shift;
+  }
+  // Whether the pieces of vectors c0 to c1 - 1 start at or after lo, and end at or before hi.
+  __device__ __forceinline__ bool after(const uint8_t* lo, int64_t c0) const { return at + c0 * BYTES >= lo; }
+  __device__ __forceinline__ bool before(const uint8_t* hi, int64_t c1) const {
+    return at + c1 * BYTES + (shift ? 16 : 0) <= hi;
+  }
+  // Starts the loads of vector c.
+  __device__ __forceinline__ Window<BYTES, RAGGED> open(int64_t c, bool want) const {
+    Window<BYTES, RAGGED> r{};
+    const uint8_t* const p = at + c * BYTES;
+    if (want) load_vec<STREAM, BYTES>(r.w, p);
+    if constexpr (RAGGED)
+      if (want && shift) load_vec<STREAM, 16>(r.w + BYTES / 4, p + BYTES);
+    return r;
+  }
+  // The vector out of its pieces.
+  __device__ __forceinline__ Words<BYTES> take(Window<BYTES, RAGGED>& v) const {
+    Words<BYTES> r;
+    if constexpr (RAGGED) {
+      const bool two = shift & 8, one = shift & 4;
+#pragma unroll
+      for (int i = 0; i < BYTES / 4 + 2; ++i) v.w[i] = two ? v.w[i + 2] : v.w[i];
+#pragma unroll
+      for (int i = 0; i < BYTES / 4 + 1; ++i) v.w[i] = one ? v.w[i + 1] : v.w[i];
+#pragma unroll
+      for (int i = 0; i < BYTES / 4; ++i) r.w[i] = __funnelshift_r(v.w[i], v.w[i + 1], 8 * (shift & 2));
+    } else {
+#pragma unroll
+      for (int i = 0; i < BYTES / 4; ++i) r.w[i] = v.w[i];
+    }
+    return r;
+  }
+};
+
+// A row of len elements, `pad` of which fit ahead of it in its first 16 bytes, as vectors c0 to c1 - 1
+// of V (vector c from element c V - pad) and as single elements: the first `head` and those from
+// `tail` on, at most 2 V - 1 of either.
+struct Split {
+  int c0, c1, head, tail, edges;
+  template <int V>
+  __device__ __forceinline__ void make(int len, int pad) {
+    c0 = pad ? 1 : 0, c1 = (len + pad) / V;
+  }
+  // Vectors whose pieces the tensor [lo, hi) does not hold whole are left to the single elements.
+  template <typename Reader>
+  __device__ __forceinline__ void clip(const Reader& in, const uint8_t* lo, const uint8_t* hi) {
+    if (!in.after(lo, c0)) ++c0;
+    if (!in.before(hi, c1)) --c1;
+  }
+  template <int V>
+  __device__ __forceinline__ void close(int len, int pad) {
+    head = min(len, c0 * V - pad);
+    tail = max(head, c1 * V - pad);
+    edges = head + len - tail;
+  }
+  __device__ __forceinline__ int column(int edge) const { return edge < head ? edge : tail + edge - head; }
+};
+
+// Elements of a row ahead of its first that its 16-byte piece holds.
+template <int EB, bool RAGGED>
+__device__ __forceinline__ int row_pad(const uint8_t* row) {
+  return RAGGED ? (int)((uintptr_t)row & 15) / EB : 0;
+}
+// Vectors of V that hold any row of len elements.
+__host__ __device__ __forceinline__ int row_vecs(int64_t len, int V, bool ragged) {
+  return (int)(ragged ? (len + 2 * V - 2) / V : len / V);
+}
+
+// Lanes that share a row of `vecs` vectors, as a power of two: four vectors each, or all lanes.  With a
+// warp for every row, the gradients of 16384 x 10 rows of 16, 64 and 256 bf16 entries took 47, 50 and
+// 71 us, so 5, 10 and 33.
+int row_lanes_log(int64_t vecs, bool ragged) {
+  int log = ragged ? 3 : 0;  // the elements at a row's ends have lanes too
+  while (log < 5 && ((int64_t)4 << log) < vecs) ++log;
+  return log;
 }
 
 template <int DT>
@@ -97,6 +167,17 @@ struct Elem {
     if (DT == SP24_BF16) return __uint_as_float(k & 1 ? word & 0xffff0000u : word << 16);
     return __half2float(__ushort_as_half((unsigned short)(k & 1 ? word >> 16 : word & 0xffffu)));
   }
+  static __device__ __forceinline__ float at(const uint8_t* row, int i) {
+    if (DT == SP24_F32) return reinterpret_cast<const float*>(row)[i];
+    const uint32_t v = reinterpret_cast<const uint16_t*>(row)[i];
+    return DT == SP24_BF16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((unsigned short)v));
+  }
+  static __device__ __forceinline__ void set(uint8_t* row, int i, float v) {
+    if (DT == SP24_F32)
+      reinterpret_cast<float*>(row)[i] = v;
+    else
+      reinterpret_cast<uint16_t*>(row)[i] = (uint16_t)bits(v);
+  }
   static __device__ __forceinline__ uint32_t bits(float v) {
     if (DT == SP24_F32) return __float_as_uint(v);
     return DT == SP24_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
@@ -107,13 +188,16 @@ struct Elem {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       if (DT == SP24_F32)
-        r.w[k] = bits(f[k]);
+        r.w[k] = __float_as_uint(f[k]);
       else if (k % 2 == 0)
-        r.w[k / 2] = bits(f[k]);
-      else
-        r.w[k / 2] |= bits(f[k]) << 16;
+        r.w[k / 2] = DT == SP24_BF16 ? pair_bits(__floats2bfloat162_rn(f[k], f[k + 1]))
+                                     : pair_bits(__floats2half2_rn(f[k], f[k + 1]));
     }
     return r;
+  }
+  template <typename P>
+  static __device__ __forceinline__ uint32_t pair_bits(P p) {
+    return *reinterpret_cast<uint32_t*>(&p);
   }
 };
 
@@ -127,7 +211,7 @@ struct Elem {
 // (one warp per expert) and its last CTA to finish adds up the experts' offsets, the third adds to
 // both the equal entries before entry i in its own chunk, and moves the rows.  At 2000 entries over 512
 // experts the first takes 7.0 us and the second 7.9, at 4000 14 and 7.9: the border is at 2048.  The
-// tables of 40960 entries take 11 us by themselves, most of it three launches; the last one's
+// tables of 40960 entries take 10 us by themselves, most of it three launches; the last one's
 // reading of keys overlaps the others' end (14 us without).
 
 struct SortTables {
@@ -150,24 +234,66 @@ __device__ __forceinline__ void put_entry(const SortTables& t, int64_t i, int ke
   t.row_expert[row] = held ? key : -1;
 }
 
-// A warp copies a row of `vecs` vectors, 8 (then 4) loads in flight per lane.
+// `lanes` lanes copy a row of `vecs` vectors, 8 (then 4) loads in flight per lane.
 template <int BYTES, int BATCH>
-__device__ __forceinline__ void copy_batches(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t vecs,
-                                             int64_t& c) {
-  for (; c + 32 * (BATCH - 1) < vecs; c += 32 * BATCH) {
+__device__ __forceinline__ void copy_batches(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int vecs,
+                                             int lanes, int& c) {
+  for (; c + lanes * (BATCH - 1) < vecs; c += lanes * BATCH) {
     Words<BYTES> v[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) v[k] = load_words<BYTES>(from, c + 32 * k);
+    for (int k = 0; k < BATCH; ++k) load_vec<false, BYTES>(v[k].w, from + (int64_t)(c + lanes * k) * BYTES);
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) store_stream<BYTES>(to, c + 32 * k, v[k]);
+    for (int k = 0; k < BATCH; ++k) store_vec(to + (int64_t)(c + lanes * k) * BYTES, v[k]);
   }
 }
 template <int BYTES>
-__device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t vecs) {
-  int64_t c = threadIdx.x & 31;
-  copy_batches<BYTES, 8>(to, from, vecs, c);
-  copy_batches<BYTES, 4>(to, from, vecs, c);
-  copy_batches<BYTES, 1>(to, from, vecs, c);
+__device__ __forceinline__ void copy_words(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t bytes,
+                                           int lanes, int sub) {
+  int c = sub;
+  const int vecs = (int)(bytes / BYTES);
+  copy_batches<BYTES, 8>(to, from, vecs, lanes, c);
+  copy_batches<BYTES, 4>(to, from, vecs, lanes, c);
+  Words<BYTES> v[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (c + lanes * k < vecs) load_vec<false, BYTES>(v[k].w, from + (int64_t)(c + lanes * k) * BYTES);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (c + lanes * k < vecs) store_vec(to + (int64_t)(c + lanes * k) * BYTES, v[k]);
+}
+__device__ __forceinline__ void copy_ragged(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t bytes,
+                                            const uint8_t* lo, const uint8_t* hi, int lanes, int sub) {
+  constexpr int kBatch = 4;
+  const int len = (int)(bytes / 2), pad = row_pad<2, true>(to);
+  RowReader<16, true, false> in;
+  in.start(from - 2 * pad);
+  Split part;
+  part.make<8>(len, pad);
+  part.clip(in, lo, hi);
+  part.close<8>(len, pad);
+  uint16_t edge = 0;  // read ahead of the vectors, written after them
+  if (sub < part.edges) edge = reinterpret_cast<const uint16_t*>(from)[part.column(sub)];
+  for (int c = part.c0 + sub; c < part.c1; c += kBatch * lanes) {
+    Window<16, true> v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) v[k] = in.open(c + k * lanes, c + k * lanes < part.c1);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (c + k * lanes < part.c1) store_vec(to - 2 * pad + (int64_t)(c + k * lanes) * 16, in.take(v[k]));
+  }
+  for (int e = sub; e < part.edges; e += lanes)
+    reinterpret_cast<uint16_t*>(to)[part.column(e)] =
+        e == sub ? edge : reinterpret_cast<const uint16_t*>(from)[part.column(e)];
+}
+// BYTES: 16, 4, or 2 for ragged rows.  FULL: all lanes of a warp (known strides: sort 35 against 37 us).
+template <int BYTES, bool FULL>
+__device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t bytes,
+                                         const uint8_t* lo, const uint8_t* hi, int lanes_log) {
+  const int lanes = FULL ? 32 : 1 << lanes_log, sub = threadIdx.x & (lanes - 1);
+  if constexpr (BYTES == 2)
+    copy_ragged(to, from, bytes, lo, hi, lanes, sub);
+  else
+    copy_words<BYTES>(to, from, bytes, lanes, sub);
 }
 
 // One warp per entry, then one per offset.
@@ -196,7 +322,8 @@ __global__ void __launch_bounds__(32 * kWarps) sort_few_kernel(const __grid_cons
     put_entry(t, i, key, before);
   }
   if (key == t.E || !x) return;
-  copy_row<BYTES>(xs + (int64_t)before * row_bytes, x + (i / topk) * row_bytes, row_bytes / BYTES);
+  copy_row<BYTES, true>(xs + (int64_t)before * row_bytes, x + (i / topk) * row_bytes, row_bytes, x,
+                   x + n / topk * row_bytes, 5);
 }
 
 // Each CTA counts one chunk, kCounters experts at a time.
@@ -283,21 +410,23 @@ __global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restr
   }
 }
 
-// kEntries entries per CTA, kParts threads each for the place within the chunk, then one warp per row
-// (64 entries of 4 threads: 44 against 41 us, too few rows under way at once).
-constexpr int kEntries = 32;
-constexpr int kParts = 8;
+// kEntries entries per CTA, kThreads / kEntries threads each for the place within the chunk, then the
+// rows, 1 << lanes_log lanes each: 32 entries where a row takes a warp (64: 44 against 41 us, too few
+// rows under way at once), 128 where rows are short or there are none.
+constexpr int kThreads = 256;
 constexpr int kMaxChunkLog = 11;
-template <int BYTES>
-__global__ void __launch_bounds__(kParts * kEntries) sort_many_kernel(const __grid_constant__ SortTables t,
-                                                                 const uint8_t* __restrict__ x, int topk,
-                                                                 int64_t row_bytes, uint8_t* __restrict__ xs) {
+template <int BYTES, int kEntries>
+__global__ void __launch_bounds__(kThreads) sort_many_kernel(const __grid_constant__ SortTables t,
+                                                             const uint8_t* __restrict__ x, int topk,
+                                                             int64_t row_bytes, uint8_t* __restrict__ xs,
+                                                             int lanes_log) {
+  constexpr int kParts = kThreads / kEntries;
   __shared__ int32_t keys[1 << kMaxChunkLog];  // from the chunk's first entry to this CTA's last
   __shared__ int rows[kEntries];
   const int64_t i0 = (int64_t)blockIdx.x * kEntries, from = i0 >> t.chunk_log << t.chunk_log;
   const int mine = (int)min((int64_t)kEntries, t.n - i0), ahead = (int)(i0 - from);
   // the keys are read before the wait: the kernel before this one, the scan, does not write them
-  for (int j = threadIdx.x; j < ahead + mine; j += kParts * kEntries) {
+  for (int j = threadIdx.x; j < ahead + mine; j += kThreads) {
     const int32_t id = t.routing[from + j];
     const int key = entry_key(id, t.E);
     if (key == t.E && id != -1 && j >= ahead) set_dev_error(SP24_ERR_INVALID_ARG);
@@ -319,9 +448,11 @@ __global__ void __launch_bounds__(kParts * kEntries) sort_many_kernel(const __gr
   }
   if (!x) return;
   __syncthreads();
-  for (int e = threadIdx.x >> 5; e < mine; e += kParts * kEntries / 32)
+  if (kEntries == 32) lanes_log = 5;
+  for (int e = threadIdx.x >> lanes_log; e < mine; e += kThreads >> lanes_log)
     if (rows[e] >= 0)
-      copy_row<BYTES>(xs + (int64_t)rows[e] * row_bytes, x + (i0 + e) / topk * row_bytes, row_bytes / BYTES);
+      copy_row<BYTES, kEntries == 32>(xs + (int64_t)rows[e] * row_bytes, x + (i0 + e) / topk * row_bytes, row_bytes, x,
+                       x + t.n / topk * row_bytes, lanes_log);
 }
 
 // Above this many entries the counts are made by chunk: see above.
@@ -354,25 +485,31 @@ __device__ __forceinline__ int entry_row(const int32_t* pos, int64_t i, int64_t 
   return -1;
 }
 
-// One warp per 32 W vectors of V columns of one token; the slots in order, kSlots of them in flight:
+// One warp (FULL) per 32 W vectors of V columns of one token, or 1 << lanes_log lanes where a row has no
+// more vectors (16384 x 10 rows of [64]: 4 against 11 us); the slots in order, kSlots of them in flight:
 // five of one vector, but two of two where a token has no more slots (16384 x 2 rows of [2048]: 31
-// against 51 us), and two of eight columns where rows allow vectors of one or two (V = 2: 34 against 39
-// us at 4096 x 10; V = 1, an odd width of a 16-bit type, takes 104 us either way).
-template <int YS, int Y, int V, int W, int kSlots>
-__global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restrict__ ys,
-                                                             const int32_t* __restrict__ pos,
-                                                             const float* __restrict__ router_w, uint32_t units,
-                                                             uint32_t per_row, int topk, int64_t rows, int64_t HV,
-                                                             void* __restrict__ y) {
-  constexpr int kIn = V * Elem<YS>::kBytes, kOut = V * Elem<Y>::kBytes;
-  const int lane = threadIdx.x & 31;
-  const uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+// against 51 us), and two of eight columns where rows allow vectors of one or two (V = 2: 31 against 39
+// us at 4096 x 10).
+template <int YS, int Y, int V, bool RAGGED, bool FULL, int W, int kSlots>
+__global__ void __launch_bounds__(32 * kWarps, !RAGGED ? 1 : YS == SP24_F32 ? 2 : 3) unsort_kernel(const uint8_t* __restrict__ ys,
+                                                                            const int32_t* __restrict__ pos,
+                                                                            const float* __restrict__ router_w,
+                                                                            uint32_t units, uint32_t per_row, int topk,
+                                                                            int64_t rows, int64_t H,
+                                                                            uint8_t* __restrict__ y, int lanes_log) {
+  constexpr int kIn = Elem<YS>::kBytes, kOut = Elem<Y>::kBytes;
+  if (FULL) lanes_log = 5;
+  const int step = 1 << lanes_log;
+  const uint32_t u = (uint32_t)(((int64_t)blockIdx.x * (32 * kWarps) + threadIdx.x) >> lanes_log);
   begin();
   if (u >= units) return;
-  const uint32_t t = u / per_row;
-  const int64_t c = (int64_t)(u - t * per_row) * (32 * W) + lane;
-  const int32_t* const my_pos = pos + (int64_t)t * topk;
-  const float* const my_w = router_w + (int64_t)t * topk;
+  const int64_t t = u / per_row;
+  const uint8_t* const end = ys + rows * H * kIn;
+  uint8_t* const row = y + t * H * kOut;
+  const int64_t c = (int64_t)(u - (uint32_t)t * per_row) * (step * W) + (threadIdx.x & (step - 1));
+  const int pad = row_pad<kOut, RAGGED>(row), vecs = (int)((H + pad + V - 1) / V);
+  const int32_t* const my_pos = pos + t * topk;
+  const float* const my_w = router_w + t * topk;
   float acc[W][V];
 #pragma unroll
   for (int j = 0; j < W; ++j)
@@ -381,7 +518,9 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restr
   for (int s0 = 0; s0 < topk; s0 += kSlots) {
     int r[kSlots];
     float w[kSlots];
-    Words<kIn> v[kSlots][W];
+    RowReader<V * kIn, RAGGED, true> in[kSlots];
+    Window<V * kIn, RAGGED> v[kSlots][W];
+    bool inside = true;
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
       const bool slot = s0 + s < topk;
@@ -390,80 +529,139 @@ __global__ void __launch_bounds__(32 * kWarps) unsort_kernel(const void* __restr
     }
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
-      const bool held = r[s] >= 0 && r[s] < rows;
-      if (!held && r[s] != -1) set_dev_error(SP24_ERR_INVALID_ARG);
-      w[s] = held ? w[s] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        v[s][j] = Words<kIn>{};
-        if (held && c + 32 * j < HV) v[s][j] = load_stream<kIn>(ys, r[s] * HV + c + 32 * j);
+      if (r[s] < 0 || r[s] >= rows) {
+        if (r[s] != -1) set_dev_error(SP24_ERR_INVALID_ARG);
+        r[s] = -1, w[s] = 0.0f;
       }
+      in[s].start(ys + (max(r[s], 0) * H - pad) * kIn);
+      // a row between others of 48 bytes or more: its pieces are in them
+      if (RAGGED && r[s] >= 0 && (r[s] == 0 || r[s] == rows - 1 || H * kIn < 48))
+        inside &= in[s].after(ys, c) && in[s].before(end, min((int64_t)vecs, c + (W - 1) * step + 1));
+    }
+    if (RAGGED && !inside) {  // a vector at an end of ys: by elements
+      for (int s = s0; s < min(s0 + kSlots, topk); ++s) {
+        const int at = my_pos[s];
+        if (at < 0 || at >= rows) continue;
+        const float weight = router_w ? my_w[s] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const int64_t i = (c + j * step) * V - pad + k;
+            if (i >= 0 && i < H) acc[j][k] = fmaf(weight, Elem<YS>::at(ys + at * H * kIn, (int)i), acc[j][k]);
+          }
+      }
+      continue;
     }
 #pragma unroll
     for (int s = 0; s < kSlots; ++s)
 #pragma unroll
-      for (int j = 0; j < W; ++j)
+      for (int j = 0; j < W; ++j) v[s][j] = in[s].open(c + j * step, r[s] >= 0 && c + j * step < vecs);
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[j][k] = fmaf(w[s], Elem<YS>::get(v[s][j], k), acc[j][k]);
+    for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const Words<V * kIn> a = in[s].take(v[s][j]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[j][k] = fmaf(w[s], Elem<YS>::get(a, k), acc[j][k]);
+      }
   }
 #pragma unroll
-  for (int j = 0; j < W; ++j)
-    if (c + 32 * j < HV) store_stream<kOut>(y, (int64_t)t * HV + c + 32 * j, Elem<Y>::put(acc[j]));
+  for (int j = 0; j < W; ++j) {
+    const int64_t i = (c + j * step) * V - pad;
+    if (RAGGED ? i >= 0 && i + V <= H : i < H)
+      store_vec(row + i * kOut, Elem<Y>::put(acc[j]));
+    else if (RAGGED && i < H)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (i + k >= 0 && i + k < H) Elem<Y>::set(row, (int)i + k, acc[j][k]);
+  }
 }
 
-// One warp per entry: its row of dys, and (DOT) the dot product that is its weight's gradient; kPairs
-// loads of either row in flight per lane.
-constexpr int kPairs = 4;
-template <int YS, int Y, int V, bool DOT>
-__global__ void __launch_bounds__(32 * kWarps) unsort_backward_kernel(
-    const void* __restrict__ dy, const void* __restrict__ ys, const int32_t* __restrict__ pos,
-    const float* __restrict__ router_w, int64_t n, int topk, int64_t rows, int64_t HV, void* __restrict__ dys,
-    float* __restrict__ d_router_w) {
-  constexpr int kIn = V * Elem<YS>::kBytes, kOut = V * Elem<Y>::kBytes;
-  const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+// 1 << lanes_log lanes per entry: its row of dys, and (DOT) the dot product that is its weight's
+// gradient; kPairs loads of either row in flight per lane.
+template <bool RAGGED>
+constexpr int kPairs = RAGGED ? 2 : 4;
+template <int YS, int Y, int V, bool RAGGED, bool DOT, bool FULL>
+__global__ void __launch_bounds__(32 * kWarps, RAGGED ? 3 : 1) unsort_backward_kernel(
+    const uint8_t* __restrict__ dy, const uint8_t* __restrict__ ys, const int32_t* __restrict__ pos,
+    const float* __restrict__ router_w, int64_t n, int topk, int64_t rows, int64_t H, uint8_t* __restrict__ dys,
+    float* __restrict__ d_router_w, int lanes_log) {
+  if (FULL) lanes_log = 5;
+  constexpr int kIn = Elem<YS>::kBytes, kOut = Elem<Y>::kBytes;
+  const int sub = threadIdx.x & ((1 << lanes_log) - 1);
+  const int64_t i = ((int64_t)blockIdx.x * (32 * kWarps) + threadIdx.x) >> lanes_log;
   begin();
-  if (i >= n) return;
-  const int r = entry_row(pos, i, rows);
-  if (r < 0) {
-    if (DOT && lane == 0) d_router_w[i] = 0.0f;
-    return;
-  }
-  const float w = router_w ? router_w[i] : 1.0f;
-  const int64_t from = (int64_t)((uint32_t)i / (uint32_t)topk) * HV, at = r * HV;
+  const int r = i < n ? entry_row(pos, i, rows) : -1;
   float dot = 0.0f;
-  auto step = [&](int64_t c, const Words<kOut>& g, const Words<kIn>& v) {
-    float d[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const float a = Elem<Y>::get(g, k);
-      if (DOT) dot = fmaf(a, Elem<YS>::get(v, k), dot);
-      d[k] = w * a;
+  if (r >= 0) {
+    const float w = router_w ? router_w[i] : 1.0f;
+    const uint8_t* const from = dy + (int64_t)((uint32_t)i / (uint32_t)topk) * H * kOut;
+    const uint8_t* const with = ys + r * H * kIn;
+    uint8_t* const to = dys + r * H * kIn;
+    const int pad = row_pad<kIn, RAGGED>(to);
+    RowReader<V * kOut, RAGGED, false> gs;
+    RowReader<V * kIn, RAGGED, true> vs;
+    gs.start(from - pad * kOut);
+    vs.start(DOT ? with - pad * kIn : nullptr);
+    Split part;
+    part.make<V>((int)H, pad);
+    float edge = 0.0f, edge_with = 0.0f;
+    if (RAGGED) {
+      part.clip(gs, dy, dy + n / topk * H * kOut);
+      if (DOT) part.clip(vs, ys, ys + rows * H * kIn);
+      part.close<V>((int)H, pad);
+      if (sub < part.edges) {  // read ahead of the vectors, used after them
+        edge = Elem<Y>::at(from, part.column(sub));
+        if (DOT) edge_with = Elem<YS>::at(with, part.column(sub));
+      }
     }
-    store_stream<kIn>(dys, at + c, Elem<YS>::put(d));
-  };
-  int64_t c = lane;
-  for (; c + 32 * (kPairs - 1) < HV; c += 32 * kPairs) {
-    Words<kOut> g[kPairs];
-    Words<kIn> v[kPairs];
+    uint8_t* const first = to - pad * kIn;
+    auto batch = [&](int c, auto all) {
+      constexpr bool ALL = decltype(all)::value;
+      Window<V * kOut, RAGGED> g[kPairs<RAGGED>];
+      Window<V * kIn, RAGGED> v[kPairs<RAGGED>];
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) {
-      g[j] = load_words<kOut>(dy, from + c + 32 * j);
-      v[j] = Words<kIn>{};
-      if (DOT) v[j] = load_stream<kIn>(ys, at + c + 32 * j);
-    }
+      for (int j = 0; j < kPairs<RAGGED>; ++j) {
+        const int at = c + (j << lanes_log);
+        g[j] = gs.open(at, ALL || at < part.c1);
+        if (DOT) v[j] = vs.open(at, ALL || at < part.c1);
+      }
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) step(c + 32 * j, g[j], v[j]);
-  }
-  for (; c < HV; c += 32) {
-    Words<kIn> v{};
-    if (DOT) v = load_stream<kIn>(ys, at + c);
-    step(c, load_words<kOut>(dy, from + c), v);
+      for (int j = 0; j < kPairs<RAGGED>; ++j) {
+        const int at = c + (j << lanes_log);
+        if (!ALL && at >= part.c1) continue;
+        const Words<V * kOut> a = gs.take(g[j]);
+        Words<V * kIn> b{};
+        if (DOT) b = vs.take(v[j]);
+        float d[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float gk = Elem<Y>::get(a, k);
+          if (DOT) dot = fmaf(gk, Elem<YS>::get(b, k), dot);
+          d[k] = w * gk;
+        }
+        store_vec(first + (int64_t)at * (V * kIn), Elem<YS>::put(d));
+      }
+    };
+    const int stride = kPairs<RAGGED> << lanes_log;
+    int c = part.c0 + sub;
+    for (; c - sub + stride <= part.c1; c += stride) batch(c, std::true_type{});
+    if (c < part.c1) batch(c, std::false_type{});
+    if (RAGGED)
+      for (int e = sub; e < part.edges; e += 1 << lanes_log) {
+        const int col = part.column(e);
+        if (e != sub) {
+          edge = Elem<Y>::at(from, col);
+          if (DOT) edge_with = Elem<YS>::at(with, col);
+        }
+        if (DOT) dot = fmaf(edge, edge_with, dot);
+        Elem<YS>::set(to, col, w * edge);
+      }
   }
   if (DOT) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
-    if (lane == 0) d_router_w[i] = dot;
+    for (int d = 1 << lanes_log >> 1; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
+    if (sub == 0 && i < n) d_router_w[i] = dot;
   }
 }
 
@@ -496,11 +694,24 @@ int vec_elems(int64_t H, const void* a, int ea, const void* b, int eb, const voi
   return 1;
 }
 
+// Calls f with the vector and whether rows are ragged (vectors of 8, where a 16-bit type has no two).
+template <int YS, int Y, typename F>
+int by_vec(int v, F f) {
+  if constexpr (YS == SP24_F32 && Y == SP24_F32) {
+    if (v == 1) return f(std::integral_constant<int, 1>{}, std::false_type{});
+  } else {
+    if (v == 8) return f(std::integral_constant<int, 8>{}, std::false_type{});
+    if (v == 1) return f(std::integral_constant<int, 8>{}, std::true_type{});
+  }
+  if (v == 4) return f(std::integral_constant<int, 4>{}, std::false_type{});
+  return f(std::integral_constant<int, 2>{}, std::false_type{});
+}
+
 int check_unsort(int ys_dtype, int y_dtype, int64_t T, int topk, int64_t rows, int64_t H) {
   if (!elem_bytes(ys_dtype) || !elem_bytes(y_dtype)) return SP24_ERR_DTYPE;
   if (ys_dtype != SP24_F32 && y_dtype != SP24_F32 && ys_dtype != y_dtype) return SP24_ERR_DTYPE;
   if (T < 0 || topk < 1 || rows < 0 || H < 0) return SP24_ERR_SHAPE;
-  if (topk > kMaxUnsortTopk || T > INT32_MAX || rows > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
+  if (topk > kMaxUnsortTopk || H > (1 << 30) || T > INT32_MAX || rows > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
   return SP24_OK;
 }
 
@@ -523,7 +734,7 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   const int eb = elem_bytes(dtype);
   if (!eb) return SP24_ERR_DTYPE;
   if (T < 0 || topk < 1 || E < 1 || H < 0) return SP24_ERR_SHAPE;
-  if (E > (1 << 16) || T > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
+  if (E > (1 << 16) || H > (1 << 30) || T > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
   const int64_t n = T * topk;
   if (!offsets || (n && (!routing || !pos || !src || !row_expert))) return SP24_ERR_INVALID_ARG;
   if (n && H && !x != !xs) return SP24_ERR_INVALID_ARG;
@@ -554,11 +765,14 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   const int64_t row = H * eb;
   const uint8_t* from = H ? reinterpret_cast<const uint8_t*>(x) : nullptr;
   uint8_t* to = reinterpret_cast<uint8_t*>(xs);
-  auto run = [&](auto bytes) {
-    constexpr int B = decltype(bytes)::value;
+  auto run = [&](auto tag) {
+    constexpr int B = decltype(tag)::value;
+    const int log = from ? row_lanes_log(row / (B == 2 ? 16 : B), B == 2) : 0;
+    if (ws.bytes && log < 5)
+      return launch_after(sort_many_kernel<B, 128>, (unsigned)((n + 127) / 128), kThreads, 0, s, t, from, topk, row, to,
+                          log);
     if (ws.bytes)
-      return launch_after(sort_many_kernel<B>, (unsigned)((n + kEntries - 1) / kEntries), kParts * kEntries, 0, s, t,
-                          from, topk, row, to);
+      return launch_after(sort_many_kernel<B, 32>, (unsigned)((n + 31) / 32), kThreads, 0, s, t, from, topk, row, to, log);
     return launch_after(sort_few_kernel<B>, (unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s, t, from, topk, row,
                         to);
   };
@@ -578,24 +792,33 @@ extern "C" int sp24_moe_unsort(const void* ys, int ys_dtype, const int32_t* pos,
   const int v = vec_elems(H, ys, ei, y, eo, nullptr, ei);
   cudaStream_t s = as_stream(stream);
   return by_pair(ys_dtype, y_dtype, [&](auto p) {
-    auto run = [&](auto vec) {
+    constexpr int YS = decltype(p)::ys, Y = decltype(p)::y;
+    return by_vec<YS, Y>(v, [&](auto vec, auto ragged) {
       constexpr int V = decltype(vec)::value;
-      auto go = [&](auto wide, auto slots) {
+      constexpr bool R = decltype(ragged)::value;
+      const int vecs = row_vecs(H, V, R);
+      auto go = [&](auto full, auto wide, auto slots, int log) {
         constexpr int W = decltype(wide)::value, S = decltype(slots)::value;
-        const int64_t per_row = (H / V + 32 * W - 1) / (32 * W), units = T * per_row;
+        const int64_t part = (int64_t)W << log, per_row = (vecs + part - 1) / part, units = T * per_row;
         if (units > INT32_MAX) return (int)SP24_ERR_UNSUPPORTED;  // more than any device's memory holds
-        return launch_after(unsort_kernel<decltype(p)::ys, decltype(p)::y, V, W, S>,
-                            (unsigned)((units + kWarps - 1) / kWarps), 32 * kWarps, 0, s, ys, pos, router_w,
-                            (uint32_t)units, (uint32_t)per_row, topk, rows, H / V, y);
+        return launch_after(unsort_kernel<YS, Y, V, R, decltype(full)::value, W, S>,
+                            (unsigned)(((units << log) + 32 * kWarps - 1) / (32 * kWarps)), 32 * kWarps, 0, s,
+                            reinterpret_cast<const uint8_t*>(ys), pos, router_w, (uint32_t)units, (uint32_t)per_row,
+                            topk, rows, H, reinterpret_cast<uint8_t*>(y), log);
       };
-      constexpr int W = V >= 4 ? 2 : 8 / V;
-      if (topk <= 2) return go(std::integral_constant<int, W>{}, std::integral_constant<int, 2>{});
-      if (V <= 2) return go(std::integral_constant<int, W>{}, std::integral_constant<int, 2>{});
-      return go(std::integral_constant<int, 1>{}, std::integral_constant<int, 5>{});
-    };
-    if (v == 8) return run(std::integral_constant<int, 8>{});
-    if (v == 4) return run(std::integral_constant<int, 4>{});
-    return v == 2 ? run(std::integral_constant<int, 2>{}) : run(std::integral_constant<int, 1>{});
+      constexpr std::integral_constant<int, 1> one{};
+      constexpr std::integral_constant<int, 2> two{};
+      constexpr std::integral_constant<int, 5> five{};
+      constexpr std::integral_constant<int, V >= 4 ? 2 : 8 / V> wide{};
+      if (vecs <= 16) {
+        int log = 0;
+        while ((1 << log) < vecs) ++log;
+        return go(std::false_type{}, one, five, log);
+      }
+      if constexpr (V <= 2) return go(std::true_type{}, wide, two, 5);
+      if (topk <= 2) return go(std::true_type{}, wide, two, 5);
+      return go(std::true_type{}, one, five, 5);
+    });
   });
 }
 
@@ -610,21 +833,23 @@ extern "C" int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void*
   if (!aligned(ys, ei) || !aligned(dys, ei) || !aligned(dy, eo) || !aligned(pos, 4) || !aligned(router_w, 4) ||
       !aligned(d_router_w, 4))
     return SP24_ERR_ALIGN;
-  const int v = vec_elems(H, ys, ei, dy, eo, dys, ei);
+  const int v = vec_elems(H, d_router_w ? ys : nullptr, ei, dy, eo, dys, ei);
   cudaStream_t s = as_stream(stream);
   const int64_t n = T * topk;
   return by_pair(ys_dtype, y_dtype, [&](auto p) {
-    auto run = [&](auto vec) {
+    constexpr int YS = decltype(p)::ys, Y = decltype(p)::y;
+    return by_vec<YS, Y>(v, [&](auto vec, auto ragged) {
       constexpr int V = decltype(vec)::value;
-      const unsigned ctas = (unsigned)((n + kWarps - 1) / kWarps);
-      if (d_router_w)
-        return launch_after(unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, true>, ctas, 32 * kWarps, 0, s, dy, ys,
-                            pos, router_w, n, topk, rows, H / V, dys, d_router_w);
-      return launch_after(unsort_backward_kernel<decltype(p)::ys, decltype(p)::y, V, false>, ctas, 32 * kWarps, 0, s, dy, ys,
-                          pos, router_w, n, topk, rows, H / V, dys, nullptr);
-    };
-    if (v == 8) return run(std::integral_constant<int, 8>{});
-    if (v == 4) return run(std::integral_constant<int, 4>{});
-    return v == 2 ? run(std::integral_constant<int, 2>{}) : run(std::integral_constant<int, 1>{});
+      constexpr bool R = decltype(ragged)::value;
+      const int log = row_lanes_log(row_vecs(H, V, R), R);
+      const int64_t ctas = ((n << log) + 32 * kWarps - 1) / (32 * kWarps);
+      auto go = [&](auto dot, auto full) {
+        return launch_after(unsort_backward_kernel<YS, Y, V, R, decltype(dot)::value, decltype(full)::value>, (unsigned)ctas, 32 * kWarps, 0, s,
+                            reinterpret_cast<const uint8_t*>(dy), reinterpret_cast<const uint8_t*>(ys), pos, router_w, n,
+                            topk, rows, H, reinterpret_cast<uint8_t*>(dys), d_router_w, log);
+      };
+      if (log == 5) return d_router_w ? go(std::true_type{}, std::true_type{}) : go(std::false_type{}, std::true_type{});
+      return d_router_w ? go(std::true_type{}, std::false_type{}) : go(std::false_type{}, std::false_type{});
+    });
   });
 }

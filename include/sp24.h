@@ -547,7 +547,7 @@ int sp24_moe_route_backward(const void* logits, int dtype, const int32_t* routin
  * x (device, F32/F16/BF16, [T, H]) and xs may both be NULL: the tables only.  Ids outside [0, E)
  * other than -1 are empty slots too and set the device error word (SP24_ERR_INVALID_ARG).
  * The gradient of x is sp24_moe_unsort of xs's gradient with router_w NULL.
- * n up to 2^31 - 1, E up to 2^16 (SP24_ERR_UNSUPPORTED above).  n == 0 writes offsets only.
+ * n up to 2^31 - 1, E up to 2^16, H up to 2^30 (SP24_ERR_UNSUPPORTED above).  n == 0 writes offsets only.
  * workspace: sp24_moe_sort_workspace_size() bytes (may be 0), 16-byte aligned; scratch. */
 int sp24_moe_sort_workspace_size(int64_t T, int topk, int64_t E, int64_t* bytes);
 int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, int64_t T, int topk, int64_t E, int64_t H,
@@ -568,7 +568,7 @@ int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, int64_t T, i
  *                                            with it)
  * A pos outside [0, rows) is an empty slot; other than -1 it sets the device error word
  * (SP24_ERR_INVALID_ARG).  Two entries of one row (no sort gives that) leave either one's dys.
- * topk up to 64 (SP24_ERR_UNSUPPORTED above).  One launch each, no workspace. */
+ * topk up to 64, H up to 2^30 (SP24_ERR_UNSUPPORTED above).  One launch each, no workspace. */
 int sp24_moe_unsort(const void* ys, int ys_dtype, const int32_t* pos, const float* router_w, int64_t T, int topk,
                     int64_t rows, int64_t H, void* y, int y_dtype, void* stream);
 int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void* ys, int ys_dtype, const int32_t* pos,

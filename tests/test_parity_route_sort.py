@@ -523,3 +523,73 @@ def test_route_weights_of_one_expert_and_extremes():
     assert not d.any()
     ids, w = sp.moe_route(l[:, :1].contiguous(), 1, sp.ROUTE_SOFTMAX, False)
     assert ids.tolist() == [[0], [0]] and w.tolist() == [[1.0], [1.0]]
+
+
+def _off(rows, H, dtype, off, fill=None, seed=0):
+    """[rows, H] that starts `off` elements behind a 256-byte boundary, and the buffer it lies in."""
+    flat = torch.full((rows * H + off + 16,), 7.0, dtype=dtype, device="cuda")
+    view = flat[off:off + rows * H].view(rows, H)
+    if fill is None:
+        view.copy_(torch.randn(rows, H, generator=torch.Generator().manual_seed(seed)))
+    return view, flat
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,k,H,a,b", [(1, 1, 1, 1, 0), (1, 1, 9, 3, 5), (5, 3, 17, 0, 1), (40, 2, 47, 7, 2), (700, 4, 16, 0, 0),
+                                       (701, 3, 24, 0, 4), (900, 3, 33, 1, 1), (1100, 2, 250, 2, 0), (690, 3, 255, 5, 6),
+                                       (1030, 2, 1001, 0, 3), (3, 2, 4099, 1, 4), (2100, 1, 8, 1, 0)])
+def test_sort_rows_of_every_start(dtype, T, k, H, a, b):
+    """Rows and tensors that start anywhere, in one launch and in three; nothing beside the rows is written."""
+    x, _ = _off(T, H, dtype, a)
+    xs, around = _off(T * k, H, dtype, b, fill=7)
+    rng = np.random.default_rng(H)
+    r = torch.from_numpy(rng.integers(-1, 9, (T, k)).astype(np.int32)).cuda()
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = sp.moe_sort(x, r, 9, out=(xs, i32(T, k), i32(T * k), i32(T * k), i32(10)))
+    want = torch.full_like(around, 7.0)
+    live = int(got.offsets[-1])
+    want[b:b + live * H] = x[(got.src[:live] // k).long()].reshape(-1)
+    assert torch.equal(around, want)
+    _cuda_ok()
+
+
+@pytest.mark.parametrize("pair", PAIRS, ids=lambda p: "-".join(str(d)[6:] for d in p))
+@pytest.mark.parametrize("T,k,H,a,b,c", [(1, 1, 1, 1, 0, 2), (2, 3, 9, 3, 5, 0), (5, 2, 16, 0, 0, 0), (9, 6, 17, 0, 1, 1),
+                                         (30, 2, 47, 7, 2, 4), (33, 7, 24, 0, 4, 8), (20, 5, 33, 1, 1, 1), (21, 3, 250, 2, 0, 6),
+                                         (7, 4, 255, 5, 6, 3), (5, 2, 1001, 0, 3, 2), (4, 6, 1001, 4, 0, 1), (2, 3, 4099, 1, 4, 5)])
+def test_unsort_rows_of_every_start(pair, T, k, H, a, b, c):
+    """The rows of ys, y, dy and dys start anywhere; nothing beside them is written."""
+    g = torch.Generator().manual_seed(T + H)
+    pos = torch.randperm(T * k, generator=g).int().view(T, k)
+    pos[T // 2, k - 1] = -1
+    w = torch.rand(T, k, generator=g)
+    pos, w = pos.cuda(), w.cuda()
+    ys, _ = _off(T * k, H, pair[0], a, seed=1)
+    y, y_around = _off(T, H, pair[1], b, fill=7)
+    dy, _ = _off(T, H, pair[1], c, seed=2)
+    dys, dys_around = _off(T * k, H, pair[0], b, fill=7)
+    # what aligned tensors of the same values give: the sums run in the same order, slot by slot
+    want = sp.moe_unsort(_whole(ys), pos, w, dtype=pair[1])[:, :H]
+    assert torch.equal(sp.moe_unsort(ys, pos, w, out=y), want)
+    live = pos[pos >= 0].long()
+    ref_dys = torch.full_like(ys, 7.0)
+    ref_dys[live] = (w[..., None] * dy[:, None].float())[pos >= 0].to(pair[0])
+    dw = torch.full((T, k), 7.0, device="cuda")
+    sp.moe_unsort_backward(dy, ys, pos, w, out=(dys, dw))
+    assert torch.equal(dys, ref_dys)
+    # a dot product of H terms in any order
+    terms = (dy[:, None].double() * ys.double()[pos.clamp(min=0).long()]) * (pos >= 0)[..., None]
+    assert ((dw.double() - terms.sum(2)).abs() <= (H + 1) * U * terms.abs().sum(2) + TINY[torch.float32]).all()
+    alone, alone_around = _off(T * k, H, pair[0], a, fill=7)
+    sp.moe_unsort_backward(dy, ys, pos, w, out=(alone, None))
+    assert torch.equal(alone, ref_dys)
+    for view, flat, b in ((y, y_around, b), (dys, dys_around, b), (alone, alone_around, a)):
+        edge = flat.clone()
+        edge[b:b + view.numel()] = 7.0
+        assert (edge == 7.0).all()
+    _cuda_ok()
+
+
+def _whole(t):
+    """t in rows of a multiple of 16 elements."""
+    return torch.nn.functional.pad(t, (0, -t.shape[1] % 16)).contiguous()

@@ -60,6 +60,13 @@ def test_unsort_refusals():
     assert g(T=0, dy=None) == sp.OK
 
 
+def test_rows_beyond_the_widest():
+    h = 2**30 + 1
+    assert _raw("sp24_moe_sort", 16, sp.BF16, 16, 4, 2, 8, h, 16, 16, 16, 16, 16, None, 0, None) == sp.ERR_UNSUPPORTED
+    assert _raw("sp24_moe_unsort", 16, sp.BF16, 16, 16, 4, 2, 8, h, 16, sp.BF16, None) == sp.ERR_UNSUPPORTED
+    assert _raw("sp24_moe_unsort_backward", 16, sp.BF16, 16, sp.BF16, 16, 16, 4, 2, 8, h, 16, 16, None) == sp.ERR_UNSUPPORTED
+
+
 def _op(scale=sp.BF16, group=128, codes=16, scales=16, zeros=None):
     return sp._W4Operand(scale, group, codes, scales, zeros)
 

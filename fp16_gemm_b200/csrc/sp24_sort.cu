@@ -206,13 +206,12 @@ struct Elem {
 // The row of entry i is the number of entries before it in the order (expert, entry number).
 //
 // Few entries: one warp per entry counts over all of them and moves the entry's row of x, in one
-// launch.  Many: three.  The entries are cut into chunks of about sqrt(n); the first launch counts
+// launch.  Many: four.  The entries are cut into chunks of about sqrt(n); the first launch counts
 // each chunk's entries per expert, the second turns an expert's counts into those of earlier chunks
 // (one warp per expert) and its last CTA to finish adds up the experts' offsets, the third adds to
-// both the equal entries before entry i in its own chunk, and moves the rows.  At 2000 entries over 512
-// experts the first takes 7.0 us and the second 7.9, at 4000 14 and 7.9: the border is at 2048.  The
-// tables of 40960 entries take 10 us by themselves, most of it three launches; the last one's
-// reading of keys overlaps the others' end (14 us without).
+// both the equal entries before entry i in its own chunk, the fourth moves the rows.  At 2000 entries over
+// 512 experts the first way takes 7.0 us and the second 8.2, at 4000 14 and 8.3: the border is at 2048.  The
+// tables take 10 us at 40960 entries and 14 at 163840, most of it launches and dependent loads.
 
 struct SortTables {
   const int32_t* routing;
@@ -285,7 +284,7 @@ __device__ __forceinline__ void copy_ragged(uint8_t* __restrict__ to, const uint
     reinterpret_cast<uint16_t*>(to)[part.column(e)] =
         e == sub ? edge : reinterpret_cast<const uint16_t*>(from)[part.column(e)];
 }
-// BYTES: 16, 4, or 2 for ragged rows.  FULL: all lanes of a warp (known strides: sort 35 against 37 us).
+// BYTES: 16, 8, 4, or 2 for ragged rows.  FULL: all lanes of a warp (known strides: sort 36 against 37 us).
 template <int BYTES, bool FULL>
 __device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t bytes,
                                          const uint8_t* lo, const uint8_t* hi, int lanes_log) {
@@ -410,49 +409,66 @@ __global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restr
   }
 }
 
-// kEntries entries per CTA, kThreads / kEntries threads each for the place within the chunk, then the
-// rows, 1 << lanes_log lanes each: 32 entries where a row takes a warp (64: 44 against 41 us, too few
-// rows under way at once), 128 where rows are short or there are none.
-constexpr int kThreads = 256;
+// One CTA per chunk: an entry's row is its expert's first, the expert's entries of earlier chunks, and
+// those of this chunk before it: the lanes of its warp with its key by a match, the warps before it by
+// counters in shared memory that the warps pass through in turn.  kCounters experts at a time.
+// (Comparing every entry with all before it in its chunk: 20 us for the tables of 163840 entries.)
+constexpr int kRankWarps = 16;
 constexpr int kMaxChunkLog = 11;
-template <int BYTES, int kEntries>
-__global__ void __launch_bounds__(kThreads) sort_many_kernel(const __grid_constant__ SortTables t,
-                                                             const uint8_t* __restrict__ x, int topk,
-                                                             int64_t row_bytes, uint8_t* __restrict__ xs,
-                                                             int lanes_log) {
-  constexpr int kParts = kThreads / kEntries;
-  __shared__ int32_t keys[1 << kMaxChunkLog];  // from the chunk's first entry to this CTA's last
-  __shared__ int rows[kEntries];
-  const int64_t i0 = (int64_t)blockIdx.x * kEntries, from = i0 >> t.chunk_log << t.chunk_log;
-  const int mine = (int)min((int64_t)kEntries, t.n - i0), ahead = (int)(i0 - from);
-  // the keys are read before the wait: the kernel before this one, the scan, does not write them
-  for (int j = threadIdx.x; j < ahead + mine; j += kThreads) {
-    const int32_t id = t.routing[from + j];
-    const int key = entry_key(id, t.E);
-    if (key == t.E && id != -1 && j >= ahead) set_dev_error(SP24_ERR_INVALID_ARG);
-    keys[j] = key;
+__global__ void __launch_bounds__(32 * kRankWarps) sort_rank_kernel(const __grid_constant__ SortTables t) {
+  extern __shared__ int32_t held[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t from = (int64_t)blockIdx.x << t.chunk_log;
+  const int mine = (int)min((int64_t)1 << t.chunk_log, t.n - from);
+  bool waited = false;
+  for (int e0 = 0; e0 <= t.E; e0 += kCounters) {
+    const int span = (int)min((int64_t)kCounters, t.E + 1 - e0);
+    for (int e = threadIdx.x; e < span; e += 32 * kRankWarps) held[e] = 0;
+    __syncthreads();
+    for (int r0 = 0; r0 < mine; r0 += 32 * kRankWarps) {
+      const int j = r0 + threadIdx.x;
+      const int32_t id = j < mine ? t.routing[from + j] : -1;
+      const int key = entry_key(id, t.E) - e0;
+      const bool in = j < mine && key >= 0 && key < span;
+      const unsigned same = __match_any_sync(kFull, in ? key : -1);
+      const int leader = __ffs(same) - 1;
+      // ids are read ahead of the wait: the kernel before this one, the scan, does not write them
+      if (!waited) begin();
+      waited = true;
+      int row = in ? t.first[e0 + key] + t.before[(e0 + key) * t.chunks + blockIdx.x] : 0;
+      int base = 0;
+      const int warps = min(kRankWarps, (mine - r0 + 31) / 32);
+      for (int w = 0; w < warps; ++w) {
+        if (w == warp && in && lane == leader) {
+          base = held[key];
+          held[key] = base + __popc(same);
+        }
+        __syncthreads();
+      }
+      base = __shfl_sync(kFull, base, leader);
+      if (in) {
+        if (e0 + key == t.E && id != -1) set_dev_error(SP24_ERR_INVALID_ARG);
+        row += base + __popc(same & ((1u << lane) - 1));
+        put_entry(t, from + j, e0 + key, row);
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int i = threadIdx.x / kParts, part = threadIdx.x % kParts;
-  const int key = i < mine ? keys[ahead + i] : 0;
-  int equal = 0;
-  if (i < mine)
-    for (int j = part; j < ahead + i; j += kParts) equal += keys[j] == key;
-#pragma unroll
-  for (int d = 1; d < kParts; d <<= 1) equal += __shfl_xor_sync(kFull, equal, d);
+}
+
+// 1 << lanes_log lanes (FULL: a warp) copy an entry's row.
+template <int BYTES, bool FULL>
+__global__ void __launch_bounds__(32 * kWarps) sort_copy_kernel(const int32_t* __restrict__ pos, int64_t n,
+                                                                const uint8_t* __restrict__ x, int topk,
+                                                                int64_t row_bytes, uint8_t* __restrict__ xs,
+                                                                int lanes_log) {
+  if (FULL) lanes_log = 5;
+  const int64_t i = ((int64_t)blockIdx.x * (32 * kWarps) + threadIdx.x) >> lanes_log;
   begin();
-  if (i < mine && part == 0) {
-    const int row = t.first[key] + t.before[key * t.chunks + (i0 >> t.chunk_log)] + equal;
-    put_entry(t, i0 + i, key, row);
-    rows[i] = key < t.E ? row : -1;
-  }
-  if (!x) return;
-  __syncthreads();
-  if (kEntries == 32) lanes_log = 5;
-  for (int e = threadIdx.x >> lanes_log; e < mine; e += kThreads >> lanes_log)
-    if (rows[e] >= 0)
-      copy_row<BYTES, kEntries == 32>(xs + (int64_t)rows[e] * row_bytes, x + (i0 + e) / topk * row_bytes, row_bytes, x,
-                       x + t.n / topk * row_bytes, lanes_log);
+  const int row = i < n ? pos[i] : -1;
+  if (row >= 0)
+    copy_row<BYTES, FULL>(xs + (int64_t)row * row_bytes, x + (int64_t)((uint32_t)i / (uint32_t)topk) * row_bytes,
+                          row_bytes, x, x + n / topk * row_bytes, lanes_log);
 }
 
 // Above this many entries the counts are made by chunk: see above.
@@ -765,18 +781,23 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
   const int64_t row = H * eb;
   const uint8_t* from = H ? reinterpret_cast<const uint8_t*>(x) : nullptr;
   uint8_t* to = reinterpret_cast<uint8_t*>(xs);
+  if (ws.bytes) {
+    const int64_t counters = E + 1 < kCounters ? E + 1 : kCounters;
+    st = launch_after(sort_rank_kernel, (unsigned)ws.chunks, 32 * kRankWarps, (size_t)counters * 4, s, t);
+    if (st || !from) return st;
+  }
   auto run = [&](auto tag) {
     constexpr int B = decltype(tag)::value;
-    const int log = from ? row_lanes_log(row / (B == 2 ? 16 : B), B == 2) : 0;
-    if (ws.bytes && log < 5)
-      return launch_after(sort_many_kernel<B, 128>, (unsigned)((n + 127) / 128), kThreads, 0, s, t, from, topk, row, to,
-                          log);
-    if (ws.bytes)
-      return launch_after(sort_many_kernel<B, 32>, (unsigned)((n + 31) / 32), kThreads, 0, s, t, from, topk, row, to, log);
-    return launch_after(sort_few_kernel<B>, (unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s, t, from, topk, row,
-                        to);
+    if (!ws.bytes)
+      return launch_after(sort_few_kernel<B>, (unsigned)((n + E + kWarps) / kWarps), 32 * kWarps, 0, s, t, from, topk, row,
+                          to);
+    const int log = row_lanes_log(row / (B == 2 ? 16 : B), B == 2);
+    const unsigned ctas = (unsigned)(((n << log) + 32 * kWarps - 1) / (32 * kWarps));
+    if (log == 5) return launch_after(sort_copy_kernel<B, true>, ctas, 32 * kWarps, 0, s, pos, n, from, topk, row, to, log);
+    return launch_after(sort_copy_kernel<B, false>, ctas, 32 * kWarps, 0, s, pos, n, from, topk, row, to, log);
   };
   if (row % 16 == 0 && aligned(x, 16) && aligned(xs, 16)) return run(std::integral_constant<int, 16>{});
+  if (row % 8 == 0 && aligned(x, 8) && aligned(xs, 8)) return run(std::integral_constant<int, 8>{});
   if (row % 4 == 0 && aligned(x, 4) && aligned(xs, 4)) return run(std::integral_constant<int, 4>{});
   return run(std::integral_constant<int, 2>{});
 }

@@ -63,7 +63,7 @@ __device__ __forceinline__ void store_vec(uint8_t* p, const Words<BYTES>& r) {
 // words ("ragged": odd widths, odd bases) are stored with aligned 16-byte vectors all the same, what is
 // ahead of the first and behind the last one by elements.  What a vector is made of is read as the
 // aligned 16-byte pieces around it and shifted, by the same amount all along a row.  4096 x 10 rows of
-// 2047 bf16 entries, against 2-byte accesses: sort 44 and 56 us, unsort 55 and 103, its gradients 84
+// 2047 bf16 entries, against 2-byte accesses: sort 46 and 56 us, unsort 55 and 103, its gradients 84
 // and 110 (what is left are the shifts' instructions; where words do, they are faster: 2046 entries,
 // unsort 34 us).
 template <int BYTES, bool RAGGED>

@@ -507,12 +507,10 @@ __device__ __forceinline__ int entry_row(const int32_t* pos, int64_t i, int64_t 
 // against 51 us), and two of eight columns where rows allow vectors of one or two (V = 2: 31 against 39
 // us at 4096 x 10).
 template <int YS, int Y, int V, bool RAGGED, bool FULL, int W, int kSlots>
-__global__ void __launch_bounds__(32 * kWarps, !RAGGED ? 1 : YS == SP24_F32 ? 2 : 3) unsort_kernel(const uint8_t* __restrict__ ys,
-                                                                            const int32_t* __restrict__ pos,
-                                                                            const float* __restrict__ router_w,
-                                                                            uint32_t units, uint32_t per_row, int topk,
-                                                                            int64_t rows, int64_t H,
-                                                                            uint8_t* __restrict__ y, int lanes_log) {
+__global__ void __launch_bounds__(32 * kWarps, !RAGGED ? 1 : YS == SP24_F32 ? 2 : 3)
+    unsort_kernel(const uint8_t* __restrict__ ys, const int32_t* __restrict__ pos, const float* __restrict__ router_w,
+                  uint32_t units, uint32_t per_row, int topk, int64_t rows, int64_t H, uint8_t* __restrict__ y,
+                  int lanes_log) {
   constexpr int kIn = Elem<YS>::kBytes, kOut = Elem<Y>::kBytes;
   if (FULL) lanes_log = 5;
   const int step = 1 << lanes_log;
@@ -727,7 +725,8 @@ int check_unsort(int ys_dtype, int y_dtype, int64_t T, int topk, int64_t rows, i
   if (!elem_bytes(ys_dtype) || !elem_bytes(y_dtype)) return SP24_ERR_DTYPE;
   if (ys_dtype != SP24_F32 && y_dtype != SP24_F32 && ys_dtype != y_dtype) return SP24_ERR_DTYPE;
   if (T < 0 || topk < 1 || rows < 0 || H < 0) return SP24_ERR_SHAPE;
-  if (topk > kMaxUnsortTopk || H > (1 << 30) || T > INT32_MAX || rows > INT32_MAX || T * topk > INT32_MAX) return SP24_ERR_UNSUPPORTED;
+  if (topk > kMaxUnsortTopk || H > (1 << 30) || T > INT32_MAX || rows > INT32_MAX || T * topk > INT32_MAX)
+    return SP24_ERR_UNSUPPORTED;
   return SP24_OK;
 }
 
@@ -793,7 +792,8 @@ extern "C" int sp24_moe_sort(const void* x, int dtype, const int32_t* routing, i
                           to);
     const int log = row_lanes_log(row / (B == 2 ? 16 : B), B == 2);
     const unsigned ctas = (unsigned)(((n << log) + 32 * kWarps - 1) / (32 * kWarps));
-    if (log == 5) return launch_after(sort_copy_kernel<B, true>, ctas, 32 * kWarps, 0, s, pos, n, from, topk, row, to, log);
+    if (log == 5)
+      return launch_after(sort_copy_kernel<B, true>, ctas, 32 * kWarps, 0, s, pos, n, from, topk, row, to, log);
     return launch_after(sort_copy_kernel<B, false>, ctas, 32 * kWarps, 0, s, pos, n, from, topk, row, to, log);
   };
   if (row % 16 == 0 && aligned(x, 16) && aligned(xs, 16)) return run(std::integral_constant<int, 16>{});
@@ -865,9 +865,9 @@ extern "C" int sp24_moe_unsort_backward(const void* dy, int y_dtype, const void*
       const int log = row_lanes_log(row_vecs(H, V, R), R);
       const int64_t ctas = ((n << log) + 32 * kWarps - 1) / (32 * kWarps);
       auto go = [&](auto dot, auto full) {
-        return launch_after(unsort_backward_kernel<YS, Y, V, R, decltype(dot)::value, decltype(full)::value>, (unsigned)ctas, 32 * kWarps, 0, s,
-                            reinterpret_cast<const uint8_t*>(dy), reinterpret_cast<const uint8_t*>(ys), pos, router_w, n,
-                            topk, rows, H, reinterpret_cast<uint8_t*>(dys), d_router_w, log);
+        return launch_after(unsort_backward_kernel<YS, Y, V, R, decltype(dot)::value, decltype(full)::value>,
+                            (unsigned)ctas, 32 * kWarps, 0, s, reinterpret_cast<const uint8_t*>(dy),
+                            reinterpret_cast<const uint8_t*>(ys), pos, router_w, n, topk, rows, H, reinterpret_cast<uint8_t*>(dys), d_router_w, log);
       };
       if (log == 5) return d_router_w ? go(std::true_type{}, std::true_type{}) : go(std::false_type{}, std::true_type{});
       return d_router_w ? go(std::true_type{}, std::false_type{}) : go(std::false_type{}, std::false_type{});

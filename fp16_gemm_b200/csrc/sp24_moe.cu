@@ -284,20 +284,35 @@ __global__ void interleave_rows_kernel(const uint4* __restrict__ a, const uint4*
 int64_t block_h_bytes(int64_t T, int topk, int64_t F) { return (T * topk * F * 2 + 15) / 16 * 16; }
 int64_t block_o_bytes(int64_t T, int topk, int64_t H) { return T * topk * H * 4; }
 
-// y[t, n] = sum_s r[t, s] * o[t, s, n], the slots in order (fp32): four outputs per thread.
-__global__ void combine_kernel(const float4* __restrict__ o, const float* __restrict__ r, int64_t T, int topk,
-                               int64_t H4, float4* __restrict__ y) {
+// y[t, n] = sum_s r[t, s] * o[t, s, n], the slots in order (fp32): four outputs per thread.  A slot
+// without an expert has no output (o is not written there) and adds nothing, whatever its weight is.
+__global__ void combine_kernel(const float4* __restrict__ o, const int32_t* __restrict__ routing,
+                               const float* __restrict__ r, int64_t T, int topk, int64_t E, int64_t H4,
+                               float4* __restrict__ y) {
+  constexpr int kAhead = 5;
   const int64_t n = T * H4;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t t = i / H4, c = i - t * H4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < topk; ++s) {
-      const float w = r[t * topk + s];
-      const float4 v = __ldcs(o + (t * topk + s) * H4 + c);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    for (int s0 = 0; s0 < topk; s0 += kAhead) {  // the loads of kAhead slots overlap, tests included
+      int32_t e[kAhead];
+      float w[kAhead];
+      float4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t at = t * topk + min(s0 + k, topk - 1);
+        e[k] = s0 + k < topk ? routing[at] : -1;
+        w[k] = r[at];
+        v[k] = __ldcs(o + at * H4 + c);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (e[k] >= 0 && e[k] < E) {
+          acc.x = fmaf(w[k], v[k].x, acc.x);
+          acc.y = fmaf(w[k], v[k].y, acc.y);
+          acc.z = fmaf(w[k], v[k].z, acc.z);
+          acc.w = fmaf(w[k], v[k].w, acc.w);
+        }
     }
     y[i] = acc;
   }
@@ -430,7 +445,7 @@ extern "C" int sp24_moe_block(const sp24_operand* x, const int32_t* routing, con
   if (st) return st;
   const int64_t nvec = T * (H / 4);
   const int64_t cb = (nvec + 255) / 256 < (int64_t)sm_count() * 8 ? (nvec + 255) / 256 : (int64_t)sm_count() * 8;
-  combine_kernel<<<(unsigned)cb, 256, 0, s>>>(reinterpret_cast<const float4*>(o), router_w, T, topk, H / 4,
-                                              reinterpret_cast<float4*>(y));
+  combine_kernel<<<(unsigned)cb, 256, 0, s>>>(reinterpret_cast<const float4*>(o), routing, router_w, T, topk, E,
+                                              H / 4, reinterpret_cast<float4*>(y));
   return launch_status();
 }

@@ -478,7 +478,9 @@ int sp24_gemm_grouped(const sp24_operand* x, const int32_t* routing, int64_t T, 
  * token t,  y[t] = sum_s r[t, s] * h_ts Wd_e^T  with  h_ts = SiLU(x_t Wg_e^T) * (x_t Wu_e^T),
  * e = routing[t, s]; SiLU(g) = g / (1 + e^-g).  h is held in x's 16-bit type; y is fp32.
  *   x          T rows of H entries, F16 or BF16, 16-byte aligned
- *   routing    device int32 [T, topk];  router_w: device fp32 [T, topk]
+ *   routing    device int32 [T, topk];  router_w: device fp32 [T, topk].  Ids outside [0, E) set
+ *              the device error word (SP24_ERR_INVALID_ARG); such a slot adds nothing to its token,
+ *              whatever its weight is
  *   w_gate_up  the E experts' gate and up weights [E * 2F, H], NVFP4, packed by
  *              sp24_interleave_rows(gate, up, block_rows = 16): rows 32k .. 32k + 15 are gate
  *              rows 16k .. 16k + 15, rows 32k + 16 .. 32k + 31 the up rows of the same features;

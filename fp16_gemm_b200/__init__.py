@@ -753,7 +753,8 @@ def grouped_workspace_bytes(T: int, topk: int, E: int) -> int:
 def gemm_grouped(x, routing: torch.Tensor, w, E: int, N: int, K: int, out=None, workspace=None,
                  stream=None) -> torch.Tensor:
     """Routed-expert GEMM: Y[t, s, :] = x[t] @ W[routing[t, s]]^T with the E experts stacked as
-    one [E*N, K] operand (16-bit tensor, NVFP4Tensor, or Sparse24 of those)."""
+    one [E*N, K] operand (16-bit tensor, NVFP4Tensor, or Sparse24 of those).  An id of -1 is a slot
+    without an expert: zeros."""
     _cuda(routing, "routing")
     T, topk = routing.shape
     dev = routing.device
@@ -829,7 +830,8 @@ def moe_block_workspace_bytes(T: int, topk: int, E: int, H: int, F: int) -> int:
 def moe_block(x: torch.Tensor, routing: torch.Tensor, router_w: torch.Tensor, w_gate_up, w_down, E: int, H: int,
               F: int, out=None, workspace=None, stream=None) -> torch.Tensor:
     """y[T, H] fp32 = sum_s r[t, s] * (SiLU(x Wg^T) * (x Wu^T)) Wd^T over the routed experts;
-    w_gate_up from pack_gate_up, w_down [E*H, F]; each an NVFP4Tensor or a Sparse24 of one."""
+    w_gate_up from pack_gate_up, w_down [E*H, F]; each an NVFP4Tensor or a Sparse24 of one.  A slot
+    with the id -1 adds nothing."""
     _cuda(routing, "routing")
     _cuda(router_w, "router_w")
     T, topk = routing.shape

@@ -23,11 +23,12 @@ namespace {
 constexpr int kTile = 64;     // token tile of the skinny kernel (the smallest tile: sizes the table)
 constexpr int kTileTc = 128;  // token tile of the tensor-core kernel
 
+// An id of -1 is a slot without an expert, any other outside [0, E) an error.
 __global__ void route_count(const int32_t* __restrict__ routing, int64_t n, int64_t E, int32_t* __restrict__ counts) {
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int32_t e = routing[i];
     if (e < 0 || e >= E) {
-      set_dev_error(SP24_ERR_INVALID_ARG);
+      if (e != -1) set_dev_error(SP24_ERR_INVALID_ARG);
       continue;
     }
     atomicAdd(&counts[e], 1);
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(1024) route_scan(const int32_t* __restrict__ c
   if (threadIdx.x == 0) *n_tiles = carry[1] < max_tiles ? carry[1] : (int32_t)max_tiles;
 }
 
-// Also zeroes the outputs of routed rows with an invalid expert id when `y_zero` is set (the
+// Also zeroes the outputs of slots without a valid expert id when `y_zero` is set (the
 // tensor-core path writes every valid output once and clears nothing else beforehand).
 __global__ void route_scatter(const int32_t* __restrict__ routing, int64_t n, int64_t E,
                               const int32_t* __restrict__ offsets, int32_t* __restrict__ fill,

@@ -457,8 +457,9 @@ int sp24_gemm_choice_reset(void);
 /* [P1] "Concurrency, not sparsity, is the lever": tokens routed top-k to E experts.
  *   Y[t, s, n] = sum_k x[t, k] W[e, n, k],  e = routing[t, s]   (fp32 [T, topk, N], device)
  *   x        T rows (F16, BF16 or NVFP4), as for sp24_gemm_dense.
- *   routing  device int32 [T, topk]; ids outside [0, E) set the device error word
- *            (SP24_ERR_INVALID_ARG) and leave their outputs 0.
+ *   routing  device int32 [T, topk]; -1 is a slot without an expert (as sp24_moe_route gives it).
+ *            Its outputs are 0, as are those of other ids outside [0, E), which set the device
+ *            error word (SP24_ERR_INVALID_ARG) too.
  *   weights  the E experts stacked as one [E*N, K] operand: exactly one of w_dense
  *            (16-bit or NVFP4; NVFP4 experts share one tensor scale, [P5] "The shared global
  *            scale") or w_sparse (2:4-compressed, stacked [E*N, K/2] values + [E*N, K/8] meta).
@@ -478,9 +479,9 @@ int sp24_gemm_grouped(const sp24_operand* x, const int32_t* routing, int64_t T, 
  * token t,  y[t] = sum_s r[t, s] * h_ts Wd_e^T  with  h_ts = SiLU(x_t Wg_e^T) * (x_t Wu_e^T),
  * e = routing[t, s]; SiLU(g) = g / (1 + e^-g).  h is held in x's 16-bit type; y is fp32.
  *   x          T rows of H entries, F16 or BF16, 16-byte aligned
- *   routing    device int32 [T, topk];  router_w: device fp32 [T, topk].  Ids outside [0, E) set
- *              the device error word (SP24_ERR_INVALID_ARG); such a slot adds nothing to its token,
- *              whatever its weight is
+ *   routing    device int32 [T, topk];  router_w: device fp32 [T, topk].  A slot with the id -1
+ *              adds nothing to its token, whatever its weight is; other ids outside [0, E) are such
+ *              slots too and set the device error word (SP24_ERR_INVALID_ARG)
  *   w_gate_up  the E experts' gate and up weights [E * 2F, H], NVFP4, packed by
  *              sp24_interleave_rows(gate, up, block_rows = 16): rows 32k .. 32k + 15 are gate
  *              rows 16k .. 16k + 15, rows 32k + 16 .. 32k + 31 the up rows of the same features;
@@ -543,7 +544,7 @@ int sp24_moe_route_backward(const void* logits, int dtype, const int32_t* routin
  *   pos         device int32 [T, topk]: the row of entry i, -1 for an empty slot (id -1)
  *   src         device int32 [n]: the entry of row r, -1 for r >= offsets[E]
  *   row_expert  device int32 [n]: the expert of row r, -1 for r >= offsets[E] (with topk = 1 the
- *               routing of sp24_gemm_grouped over xs when no slot is empty)
+ *               routing of sp24_gemm_grouped over xs)
  *   xs          device [n, H], x's type: xs[r] = x[src[r] / topk]; rows r >= offsets[E] are left as
  *               they were.
  * x (device, F32/F16/BF16, [T, H]) and xs may both be NULL: the tables only.  Ids outside [0, E)

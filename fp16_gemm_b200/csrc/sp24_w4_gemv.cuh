@@ -27,6 +27,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, const u
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// A bounded wait of the whole warp.  Each lane measures its own time: where the limit falls next to the
+// barrier's completion some find it run out and others not, so they agree, and all give up or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFull, tc::mbar_wait(bar, parity));
+}
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -298,8 +303,11 @@ struct Walk {
 // XW: x stands in shared memory whole, its pairs picked when it is brought there; otherwise (experts,
 // or a large x) it is read from global memory half a chunk ahead and its pairs are picked at each use.
 //
-// Waits are bounded by the library's wait limit: a warp that gives up records it, does not wait again
-// and passes through the rest of its items, so every barrier is still met.
+// Waits are bounded by the library's wait limit, and a warp's lanes give up together.  A multiplying
+// warp that gives up records it, does not wait again and passes through the rest of its items, so
+// every barrier of its team is still met.  A copying warp records it, waits for its copies in flight
+// and ends: it meets no barrier of a team, and the multiplying warps that wait for its next stage give
+// up in turn.
 template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW, bool ZEROS, int GB>
 struct GemvKernel {
   static constexpr int kTok = 8 * NT;
@@ -405,7 +413,7 @@ struct GemvKernel {
       auto row_of = [&](int r) { return SWIGLU ? (r & 15) + (r >> 5) * 16 : r; };  // within the item
 
       for (int k0 = k_first; k0 < K; k0 += k_step) {
-        if (round && !tc::mbar_wait(bars + 2 * stage + 1, (round - 1) & 1)) {
+        if (round && !warp_wait(bars + 2 * stage + 1, (round - 1) & 1)) {
           set_dev_error(SP24_ERR_DEVICE_TIMEOUT);
           copy_wait_all();
           return;
@@ -616,11 +624,10 @@ struct GemvKernel {
         const uint32_t at = stage * kStage;
         uint4 x[2][NT][kAhead];
         read_x(x[0], k, 0, blocks);
-        if (!given_up && !tc::mbar_wait(bars + 2 * stage, parity)) {
+        if (!given_up && !warp_wait(bars + 2 * stage, parity)) {
           set_dev_error(SP24_ERR_DEVICE_TIMEOUT);
           given_up = true;
         }
-        __syncwarp();
         if (blocks == kChunk / 32) {  // a whole chunk: straight through
 #pragma unroll
           for (int part = 0; part < kParts; ++part) {

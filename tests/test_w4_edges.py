@@ -1,0 +1,48 @@
+"""Edges of the 4-bit products: waits that run out in every form."""
+import contextlib
+import ctypes
+
+import pytest
+import torch
+
+import fp16_gemm_b200 as sp
+from test_parity_w4 import _cuda_ok, _gen, random_w4
+
+
+@contextlib.contextmanager
+def _wait_limit(ns):
+    old = ctypes.c_ulonglong()
+    assert sp.lib().sp24_get_wait_limit(ctypes.byref(old)) == sp.OK
+    assert sp.lib().sp24_set_wait_limit(ns) == sp.OK
+    try:
+        yield
+    finally:
+        assert sp.lib().sp24_set_wait_limit(old.value) == sp.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [sp.ACT_NONE, sp.ACT_SWIGLU], ids=["none", "swiglu"])
+@pytest.mark.parametrize("form", ["many items", "shared K", "x outside", "experts", "experts, shared K"])
+def test_waits_that_run_out(form, act):
+    """With a wait limit that most waits outlast, a call ends, and its result is right or it is
+    reported; the next call is right."""
+    dtype = torch.bfloat16
+    M, N, K, E = {"many items": (2, 20000, 4096, 0), "shared K": (12, 48, 11232, 0), "x outside": (16, 9000, 9088, 0),
+                  "experts": (70, 1024, 2048, 40), "experts, shared K": (5, 32, 9088, 3)}[form]
+    x = torch.randn(M, K, generator=_gen(1)).to(dtype).cuda()
+    w = random_w4(max(E, 1) * N, K, 32, True, dtype, 2)
+    if E:
+        counts = torch.randint(0, E, (M,), generator=_gen(3)).bincount(minlength=E)
+        offsets = torch.cat((torch.zeros(1, dtype=torch.int64), counts.cumsum(0))).int().cuda()
+        call = lambda: sp.gemv_w4_grouped(x, w, offsets, act)  # noqa: E731
+    else:
+        call = lambda: sp.gemv_w4(x, w, act)  # noqa: E731
+    want = call()
+    _cuda_ok()
+    for limit in (1, 200, 1000, 3000):
+        with _wait_limit(limit):
+            y = call()
+            status = sp.last_device_error()
+        assert status == sp.ERR_DEVICE_TIMEOUT or (status == sp.OK and torch.equal(y, want))
+    assert torch.equal(call(), want)
+    _cuda_ok()

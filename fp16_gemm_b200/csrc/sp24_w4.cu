@@ -207,8 +207,9 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   const int yb = elem_bytes(y_dtype);
   if (!y || (grouped && !offsets)) return SP24_ERR_INVALID_ARG;
   if (!aligned(y, yb) || !aligned(offsets, 4)) return SP24_ERR_ALIGN;
-  if (K == 0) return cudaMemsetAsync(y, 0, (size_t)(M * cols * yb), s) == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
-  if (!x || !w->codes || !w->scales) return SP24_ERR_INVALID_ARG;
+  // with experts the kernel runs for K == 0 too (it reads offsets alone): only their rows are cleared
+  if (K == 0 && !grouped) return cudaMemsetAsync(y, 0, (size_t)(M * cols * yb), s) == cudaSuccess ? SP24_OK : SP24_ERR_CUDA;
+  if (K && (!x || !w->codes || !w->scales)) return SP24_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 16) || !aligned(w->zeros, 16)) return SP24_ERR_ALIGN;
   const GemvW4 p{x, w->codes, reinterpret_cast<const uint16_t*>(w->scales), w->zeros, grouped ? offsets : nullptr, y,
                  M, E, N, K, w->scale_dtype, w->group, y_dtype == SP24_F32, 1};

@@ -626,7 +626,8 @@ int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_t K, int ou
  * Any number of rows is served, up to sixteen per read of a weight tile: for more than a few dozen
  * rows use the GEMM entry points.  K up to 2^24 and E up to 2^20
  * (SP24_ERR_UNSUPPORTED above).  M == 0,
- * R == 0 or N == 0 is a no-op; K == 0 writes zeros.  One launch, no workspace, no atomics. */
+ * R == 0 or N == 0 is a no-op; K == 0 writes zeros (over experts in their rows only).  One launch, no
+ * workspace, no atomics. */
 enum { SP24_ACT_NONE = 0, SP24_ACT_SWIGLU = 1 };
 int sp24_gemv_w4(const void* x, int x_dtype, const sp24_w4_operand* w, int64_t M, int64_t N, int64_t K, int act,
                  void* y, int y_dtype, void* stream);

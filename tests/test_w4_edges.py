@@ -1,4 +1,4 @@
-"""Edges of the 4-bit products: waits that run out in every form."""
+"""Edges of the 4-bit products: waits that run out in every form, experts over no entries."""
 import contextlib
 import ctypes
 
@@ -46,3 +46,21 @@ def test_waits_that_run_out(form, act):
         assert status == sp.ERR_DEVICE_TIMEOUT or (status == sp.OK and torch.equal(y, want))
     assert torch.equal(call(), want)
     _cuda_ok()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [sp.ACT_NONE, sp.ACT_SWIGLU], ids=["none", "swiglu"])
+@pytest.mark.parametrize("N", [2, 34, 3000])
+@pytest.mark.parametrize("at", [[1, 4, 4, 6], [0, 30, 60, 61], [0, 0, 0, 0], [-3, 2, 70, 99]])
+def test_experts_over_no_entries_write_only_their_rows(at, N, act):
+    """K = 0: zeros in the rows that an expert has, the others as they were."""
+    R, E = 64, 3
+    none = sp.W4Tensor(torch.empty(E * N, 0, dtype=torch.uint8, device="cuda"),
+                       torch.empty(E * N, 0, dtype=torch.bfloat16, device="cuda"))
+    out = torch.full((R, N // 2 if act else N), -5.0, device="cuda")
+    sp.gemv_w4_grouped(torch.empty(R, 0, dtype=torch.bfloat16, device="cuda"), none,
+                       torch.tensor(at, dtype=torch.int32, device="cuda"), act, out=out)
+    _cuda_ok()
+    want = torch.full_like(out, -5.0)
+    want[max(at[0], 0):min(at[-1], R)] = 0.0
+    assert torch.equal(out, want)

@@ -28,6 +28,7 @@ struct GemvW4 {
   void* y;
   int64_t M, E, N, K;
   int scale_dtype, group, y_f32;
+  int tile_bound;  // set by the launch, with experts: the most row tiles that ascending offsets give
   int share;  // set by the launch: the teams of a CTA that take an item's K together, all or one
 };
 

@@ -139,64 +139,85 @@ __device__ __forceinline__ void expert_rows(const GemvW4& p, int e, int& first, 
   }
 }
 
+// Numbers of tiles.  Offsets that ascend give at most M / STEP and one per expert that has rows, which
+// the launch knows (p.tile_bound) and keeps below kManyTiles.  Others may name the same rows again and
+// again: sums stop at kManyTiles instead of wrapping, and tiles from the bound on are left out.
+constexpr unsigned kManyTiles = 1u << 30;
+
+template <int STEP>
+__device__ __forceinline__ unsigned tiles_of(int first, int end) {
+  return ((unsigned)(end - first) + STEP - 1) / STEP;
+}
+
+// The lanes' sum; each has kManyTiles at most.
+__device__ __forceinline__ unsigned sum_tiles(unsigned v) {
+  const uint64_t all =
+      ((uint64_t)__reduce_add_sync(kFull, v >> 16) << 16) + __reduce_add_sync(kFull, v & 0xffffu);
+  return (unsigned)min(all, (uint64_t)kManyTiles);
+}
+
 // Inclusive sum over the lanes.
-__device__ __forceinline__ int warp_scan(int v) {
+__device__ __forceinline__ unsigned scan_tiles(unsigned v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(kFull, v, d);
-    if (lane >= d) v += o;
+    const unsigned o = __shfl_up_sync(kFull, v, d);
+    if (lane >= d) v = min(v + o, kManyTiles);
   }
   return v;
 }
 
 // The tiles of experts 32 b .. 32 b + 31.
 template <int STEP>
-__device__ __forceinline__ int block_tiles(const GemvW4& p, int b) {
+__device__ __forceinline__ unsigned block_tiles(const GemvW4& p, int b) {
   int first, end;
   expert_rows(p, 32 * b + (threadIdx.x & 31), first, end);
-  return __reduce_add_sync(kFull, (end - first + STEP - 1) / STEP);
+  return sum_tiles(tiles_of<STEP>(first, end));
 }
 
 // A CTA's warps share the counting: `table` holds block_tiles of the first kBlocks blocks.
 constexpr int kBlocks = 192;
 
 template <int STEP, typename F>
-__device__ __forceinline__ void each_32_blocks(const GemvW4& p, const int* table, F f) {
+__device__ __forceinline__ void each_32_blocks(const GemvW4& p, const unsigned* table, F f) {
   const int lane = threadIdx.x & 31, blocks = (int)((p.E + 31) / 32);
   for (int b0 = 0; b0 < blocks; b0 += 32) {
-    int mine = b0 + lane < min(blocks, kBlocks) ? table[b0 + lane] : 0;
+    unsigned mine = b0 + lane < min(blocks, kBlocks) ? table[b0 + lane] : 0;
     for (int b = max(b0, kBlocks); b < min(blocks, b0 + 32); ++b) {  // experts that the table has no room for
-      const int s = block_tiles<STEP>(p, b);
+      const unsigned s = block_tiles<STEP>(p, b);
       if (b == b0 + lane) mine = s;
     }
     if (f(b0, mine)) return;
   }
 }
 
+// The tiles that are walked: all of them, up to the bound.
 template <int STEP>
-__device__ __forceinline__ int count_tiles(const GemvW4& p, const int* table) {
-  int mine = 0;
-  each_32_blocks<STEP>(p, table, [&](int, int tiles) {
-    mine += tiles;
+__device__ __forceinline__ int count_tiles(const GemvW4& p, const unsigned* table) {
+  unsigned mine = 0;
+  each_32_blocks<STEP>(p, table, [&](int, unsigned tiles) {
+    mine = min(mine + tiles, kManyTiles);
     return false;
   });
-  return __reduce_add_sync(kFull, mine);
+  const unsigned all = sum_tiles(mine), bound = p.tile_bound;
+  if (all > bound && (threadIdx.x & 31) == 0) set_dev_error(SP24_ERR_INVALID_ARG);
+  return (int)min(all, bound);
 }
 
 // Tile number `tile`, which is below the count.
 template <int STEP>
-__device__ __forceinline__ TokenTile find_tile(const GemvW4& p, const int* table, int tile) {
+__device__ __forceinline__ TokenTile find_tile(const GemvW4& p, const unsigned* table, unsigned tile) {
   const int lane = threadIdx.x & 31;
   TokenTile t{0, 0, 0};
   // the lane whose tiles the wanted one is among; the tiles before that lane's are taken off
-  auto pick = [&](int tiles) {
-    const int upto = warp_scan(tiles), l = __ffs(__ballot_sync(kFull, upto > tile)) - 1;
-    if (l >= 0) tile -= __shfl_sync(kFull, upto - tiles, l);
+  auto pick = [&](unsigned tiles) {
+    const unsigned upto = scan_tiles(tiles);
+    const int l = __ffs(__ballot_sync(kFull, upto > tile)) - 1;
+    if (l > 0) tile -= __shfl_sync(kFull, upto, l - 1);
     return l;
   };
-  each_32_blocks<STEP>(p, table, [&](int b0, int tiles) {
-    const int here = __reduce_add_sync(kFull, tiles);
+  each_32_blocks<STEP>(p, table, [&](int b0, unsigned tiles) {
+    const unsigned here = sum_tiles(tiles);
     if (tile >= here) {
       tile -= here;
       return false;
@@ -204,8 +225,8 @@ __device__ __forceinline__ TokenTile find_tile(const GemvW4& p, const int* table
     const int e0 = 32 * (b0 + pick(tiles));
     int first, end;
     expert_rows(p, e0 + lane, first, end);
-    const int l = pick((end - first + STEP - 1) / STEP);
-    t = {e0 + l, __shfl_sync(kFull, first, l) + tile * STEP, __shfl_sync(kFull, end, l)};
+    const int l = pick(tiles_of<STEP>(first, end));
+    t = {e0 + l, __shfl_sync(kFull, first, l) + (int)tile * STEP, __shfl_sync(kFull, end, l)};
     return true;
   });
   return t;
@@ -238,14 +259,14 @@ struct Walk {
   int col;    // column tile
   TokenTile tok;
 
-  __device__ __forceinline__ void start(const GemvW4& p, const int* table, int col_tiles, int team, int teams) {
+  __device__ __forceinline__ void start(const GemvW4& p, const unsigned* table, int col_tiles, int team, int teams) {
     if (p.offsets) {
       const int64_t all = (int64_t)count_tiles<STEP>(p, table) * col_tiles;
       const int64_t first = all * team / teams;
       left = (int)(all * (team + 1) / teams - first);
       if (left <= 0) return;
       col = (int)(first % col_tiles);
-      tok = find_tile<STEP>(p, table, (int)(first / col_tiles));
+      tok = find_tile<STEP>(p, table, (unsigned)(first / col_tiles));
     } else {
       const int tiles = (int)((p.M + STEP - 1) / STEP), all = tiles * col_tiles;
       item = team;
@@ -350,7 +371,7 @@ struct GemvKernel {
       }
       tc::fence_mbar_init();
     }
-    int* const table = reinterpret_cast<int*>(smem + kTableAt);
+    unsigned* const table = reinterpret_cast<unsigned*>(smem + kTableAt);
     begin();
     if (p.offsets)
       for (int b = warp; b < min((int)((p.E + 31) / 32), kBlocks); b += kMulWarps + kTeams) table[b] = block_tiles<kTok>(p, b);
@@ -374,7 +395,7 @@ struct GemvKernel {
   }
 
   // ---- the copying warp: lane l copies piece l & 7 of rows (l >> 3) + 4 h of each of the four chunks
-  static __device__ __forceinline__ void copy(const GemvW4& p, const int* table, uint8_t* ring, uint64_t* bars, int team,
+  static __device__ __forceinline__ void copy(const GemvW4& p, const unsigned* table, uint8_t* ring, uint64_t* bars, int team,
                                               int teams, int k_first, int k_step) {
     const int lane = threadIdx.x & 31;
     const int64_t cols = columns(p);
@@ -513,7 +534,7 @@ struct GemvKernel {
     }
 
     Walk<kTok> walk;
-    walk.start(p, reinterpret_cast<const int*>(smem + kTableAt), col_tiles, team, teams);
+    walk.start(p, reinterpret_cast<const unsigned*>(smem + kTableAt), col_tiles, team, teams);
     // ldmatrix: lane l names row (l & 7) + 8 (l >> 3 & 1) of block (l >> 4); block j + 2 n: ^ 32 n
     const int lm_row = (lane & 7) + 8 * (lane >> 3 & 1);
     const uint32_t lm_at = smem_addr(ring) + in_team * (MT * kTileBytes) + lm_row * 128 + 16 * ((lane >> 4) ^ (lane & 7));
@@ -715,6 +736,7 @@ int launch_gemv(GemvW4 p, cudaStream_t s) {
   const int64_t tok_tiles = (p.M + Kern::kTok - 1) / Kern::kTok + (p.offsets ? (p.E < p.M ? p.E : p.M) : 0);
   const int64_t items = col_tiles * tok_tiles;
   if (items > INT32_MAX / 2) return SP24_ERR_UNSUPPORTED;
+  p.tile_bound = (int)tok_tiles;
   // Few items: the four teams of a CTA take the K of one together.  The cost is rounds of items times
   // steps of K and about one for an item's ends (12 rows through [48, 11232], groups of 32 with zero
   // points: 15 us shared, 23 alone).

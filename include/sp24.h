@@ -616,7 +616,10 @@ int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_t K, int ou
  *   sp24_gemv_w4_grouped  x device [R, K] in expert order, E matrices stacked as [E N, K], offsets
  *                         device int32 [E + 1] (sp24_moe_sort): row r in [offsets[e], offsets[e+1])
  *                         meets matrix e; rows of y from offsets[E] on are left as they were.
- *                         Offsets are clamped to [0, R]; a descending pair holds no rows.
+ *                         Offsets are clamped to [0, R]; a descending pair holds no rows.  Offsets
+ *                         that name rows so often that they exceed what R rows can need (R / 8
+ *                         tiles of rows and one for each expert, or row, whichever are fewer) set
+ *                         the device error word (SP24_ERR_INVALID_ARG), and y is unspecified.
  *   x     F16 or BF16, 16-byte aligned; scale_dtype may be the other one of the two.
  *   act   SP24_ACT_NONE:   y[m, n] = v[m, n], y [M, N]
  *         SP24_ACT_SWIGLU: N even, the first N/2 rows of a matrix are the gate, the others the up

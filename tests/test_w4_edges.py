@@ -64,3 +64,32 @@ def test_experts_over_no_entries_write_only_their_rows(at, N, act):
     want = torch.full_like(out, -5.0)
     want[max(at[0], 0):min(at[-1], R)] = 0.0
     assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,R", [(64, 100), (64, 3), (7000, 300), (4096, 1 << 25), (1 << 20, 65600)])
+def test_offsets_that_name_rows_again_and_again(E, R):
+    """Every other expert holds all rows: more tiles than any sorted rows have, in the larger cases more
+    than 32 bits count.  The call ends soon, reports it and writes nothing beside y."""
+    K = N = 32
+    if R * E > 1 << 30:
+        N = 1
+    w = random_w4(64, K, 32, False, torch.float16, 1)
+    w = sp.W4Tensor(w.codes[:N].repeat(E, 1), w.scales[:N].repeat(E, 1))
+    x = torch.zeros(R, K, dtype=torch.float16, device="cuda")
+    around = torch.full((R + 2, N), -5.0, device="cuda")
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = R
+    sp.gemv_w4_grouped(x, w, offsets, out=around[1:-1])
+    torch.cuda.synchronize()
+    assert sp.last_device_error() == sp.ERR_INVALID_ARG
+    assert (around[0] == -5).all() and (around[-1] == -5).all()
+    # every row is the first expert's too, and every expert here is the same
+    assert not around[1:-1].any()
+    # the last expert alone has them: nothing is reported, and all are there
+    offsets.zero_()
+    offsets[-1] = R
+    around[1:-1] = -5.0
+    sp.gemv_w4_grouped(x, w, offsets, out=around[1:-1])
+    _cuda_ok()
+    assert not around[1:-1].any() and (around[0] == -5).all() and (around[-1] == -5).all()

@@ -1,9 +1,13 @@
 // Programmatic dependent launch: the kernels that are launched with launch_after start while their
 // predecessor in the stream is still ending, so that a launch's latency and a kernel's set-up are
-// hidden behind it.  Such a kernel calls begin() in every thread before it touches global memory: it waits, in
-// hardware, until its predecessor has ended and its writes are visible, and then lets its own successor
-// start.  In this order a kernel that has started knows that all before its predecessor has ended, and
-// may read what the predecessor alone does not write.
+// hidden behind it.  Such a kernel calls begin() in every thread, once, before it touches global memory:
+// it waits, in hardware, until its predecessor has ended and its writes are visible, and then lets its own
+// successor start (whose predecessor's predecessor has ended then).
+//
+// What such a kernel reads may be written while it already runs, and what it writes may still be read.
+// So no load takes the read-only path (__ldg, ld.global.nc: defined for data that nobody writes while the
+// kernel runs), and no pointer is __restrict__: the compiler may choose that path for one that is only
+// read, and need not keep accesses through any of them behind begin().
 #pragma once
 
 #include "sp24_internal.cuh"
@@ -13,6 +17,15 @@ namespace sp24 {
 __device__ __forceinline__ void begin() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Sixteen bytes that are read once: they do not displace others in L1.
+__device__ __forceinline__ uint4 load_stream16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
 }
 
 template <typename... P, typename... A>

@@ -60,10 +60,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
 template <int DT, int NV>
-__global__ void __launch_bounds__(kThreads) route_topk_kernel(const void* __restrict__ logits, int64_t T, int E,
+__global__ void __launch_bounds__(kThreads) route_topk_kernel(const void* logits, int64_t T, int E,
                                                               int topk, int scoring, int renorm,
-                                                              int32_t* __restrict__ routing,
-                                                              float* __restrict__ router_w) {
+                                                              int32_t* routing,
+                                                              float* router_w) {
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   begin();
@@ -176,11 +176,11 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const void* __rest
 }
 
 template <int DT, int NV>
-__global__ void __launch_bounds__(kThreads) route_backward_kernel(const void* __restrict__ logits, int64_t T, int E,
+__global__ void __launch_bounds__(kThreads) route_backward_kernel(const void* logits, int64_t T, int E,
                                                                   int topk, int scoring, int renorm,
-                                                                  const int32_t* __restrict__ routing,
-                                                                  const float* __restrict__ d_router_w,
-                                                                  void* __restrict__ dlogits) {
+                                                                  const int32_t* routing,
+                                                                  const float* d_router_w,
+                                                                  void* dlogits) {
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   begin();

@@ -15,6 +15,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 8;
 constexpr int kMaxUnsortTopk = 64;
 constexpr int kCounters = 8192;  // counters of one pass over a chunk (32 KB of shared memory)
+constexpr int kMaxChunkLog = 11;
 
 // ------------------------------------------------------------------ element access
 
@@ -235,7 +236,7 @@ __device__ __forceinline__ void put_entry(const SortTables& t, int64_t i, int ke
 
 // `lanes` lanes copy a row of `vecs` vectors, 8 (then 4) loads in flight per lane.
 template <int BYTES, int BATCH>
-__device__ __forceinline__ void copy_batches(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int vecs,
+__device__ __forceinline__ void copy_batches(uint8_t* to, const uint8_t* from, int vecs,
                                              int lanes, int& c) {
   for (; c + lanes * (BATCH - 1) < vecs; c += lanes * BATCH) {
     Words<BYTES> v[BATCH];
@@ -246,7 +247,7 @@ __device__ __forceinline__ void copy_batches(uint8_t* __restrict__ to, const uin
   }
 }
 template <int BYTES>
-__device__ __forceinline__ void copy_words(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t bytes,
+__device__ __forceinline__ void copy_words(uint8_t* to, const uint8_t* from, int64_t bytes,
                                            int lanes, int sub) {
   int c = sub;
   const int vecs = (int)(bytes / BYTES);
@@ -260,7 +261,7 @@ __device__ __forceinline__ void copy_words(uint8_t* __restrict__ to, const uint8
   for (int k = 0; k < 3; ++k)
     if (c + lanes * k < vecs) store_vec(to + (int64_t)(c + lanes * k) * BYTES, v[k]);
 }
-__device__ __forceinline__ void copy_ragged(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t bytes,
+__device__ __forceinline__ void copy_ragged(uint8_t* to, const uint8_t* from, int64_t bytes,
                                             const uint8_t* lo, const uint8_t* hi, int lanes, int sub) {
   constexpr int kBatch = 4;
   const int len = (int)(bytes / 2), pad = row_pad<2, true>(to);
@@ -286,7 +287,7 @@ __device__ __forceinline__ void copy_ragged(uint8_t* __restrict__ to, const uint
 }
 // BYTES: 16, 8, 4, or 2 for ragged rows.  FULL: all lanes of a warp (known strides: sort 36 against 37 us).
 template <int BYTES, bool FULL>
-__device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t* __restrict__ from, int64_t bytes,
+__device__ __forceinline__ void copy_row(uint8_t* to, const uint8_t* from, int64_t bytes,
                                          const uint8_t* lo, const uint8_t* hi, int lanes_log) {
   const int lanes = FULL ? 32 : 1 << lanes_log, sub = threadIdx.x & (lanes - 1);
   if constexpr (BYTES == 2)
@@ -298,8 +299,8 @@ __device__ __forceinline__ void copy_row(uint8_t* __restrict__ to, const uint8_t
 // One warp per entry, then one per offset.
 template <int BYTES>
 __global__ void __launch_bounds__(32 * kWarps) sort_few_kernel(const __grid_constant__ SortTables t,
-                                                               const uint8_t* __restrict__ x, int topk,
-                                                               int64_t row_bytes, uint8_t* __restrict__ xs) {
+                                                               const uint8_t* x, int topk,
+                                                               int64_t row_bytes, uint8_t* xs) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * kWarps + (threadIdx.x >> 5), n = (int)t.n;
   begin();
@@ -326,21 +327,27 @@ __global__ void __launch_bounds__(32 * kWarps) sort_few_kernel(const __grid_cons
 }
 
 // Each CTA counts one chunk, kCounters experts at a time.
-__global__ void __launch_bounds__(256) sort_count_kernel(const int32_t* __restrict__ routing, int64_t n, int64_t E,
-                                                         int chunk_log, int64_t chunks, int32_t* __restrict__ counts,
-                                                         int32_t* __restrict__ done) {
+__global__ void __launch_bounds__(256) sort_count_kernel(const int32_t* routing, int64_t n, int64_t E,
+                                                         int chunk_log, int64_t chunks, int32_t* counts,
+                                                         int32_t* done) {
   extern __shared__ int32_t held[];
   begin();
   if (blockIdx.x == 0 && threadIdx.x == 0) *done = 0;
+  constexpr int kEach = (1 << kMaxChunkLog) / 256;
   const int64_t from = (int64_t)blockIdx.x << chunk_log, to = min(n, from + ((int64_t)1 << chunk_log));
+  int key[kEach];  // a thread's entries, all loads in flight together
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int64_t j = from + threadIdx.x + 256 * k;
+    key[k] = j < to ? entry_key(routing[j], E) : -1;
+  }
   for (int e0 = 0; e0 <= E; e0 += kCounters) {
     const int span = (int)min((int64_t)kCounters, E + 1 - e0);
     for (int e = threadIdx.x; e < span; e += 256) held[e] = 0;
     __syncthreads();
-    for (int64_t j = from + threadIdx.x; j < to; j += 256) {
-      const int key = entry_key(routing[j], E) - e0;
-      if (key >= 0 && key < span) atomicAdd(&held[key], 1);
-    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (key[k] >= e0 && key[k] - e0 < span) atomicAdd(&held[key[k] - e0], 1);
     __syncthreads();
     for (int e = threadIdx.x; e < span; e += 256) counts[(int64_t)(e0 + e) * chunks + blockIdx.x] = held[e];
     __syncthreads();
@@ -361,10 +368,10 @@ __device__ __forceinline__ int warp_scan(int v) {
 
 // One warp per expert: its counts become those of earlier chunks.  The CTA that finishes last (a
 // counter tells; nobody waits) turns the totals into `first` and the offsets.
-__global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restrict__ counts, int64_t E, int64_t chunks,
-                                                                int32_t* __restrict__ first,
-                                                                int32_t* __restrict__ offsets,
-                                                                int32_t* __restrict__ done) {
+__global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* counts, int64_t E, int64_t chunks,
+                                                                int32_t* first,
+                                                                int32_t* offsets,
+                                                                int32_t* done) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t e = (int64_t)blockIdx.x * kWarps + warp;
   begin();
@@ -414,7 +421,6 @@ __global__ void __launch_bounds__(32 * kWarps) sort_scan_kernel(int32_t* __restr
 // counters in shared memory that the warps pass through in turn.  kCounters experts at a time.
 // (Comparing every entry with all before it in its chunk: 20 us for the tables of 163840 entries.)
 constexpr int kRankWarps = 16;
-constexpr int kMaxChunkLog = 11;
 __global__ void __launch_bounds__(32 * kRankWarps) sort_rank_kernel(const __grid_constant__ SortTables t) {
   extern __shared__ int32_t held[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -458,9 +464,9 @@ __global__ void __launch_bounds__(32 * kRankWarps) sort_rank_kernel(const __grid
 
 // 1 << lanes_log lanes (FULL: a warp) copy an entry's row.
 template <int BYTES, bool FULL>
-__global__ void __launch_bounds__(32 * kWarps) sort_copy_kernel(const int32_t* __restrict__ pos, int64_t n,
-                                                                const uint8_t* __restrict__ x, int topk,
-                                                                int64_t row_bytes, uint8_t* __restrict__ xs,
+__global__ void __launch_bounds__(32 * kWarps) sort_copy_kernel(const int32_t* pos, int64_t n,
+                                                                const uint8_t* x, int topk,
+                                                                int64_t row_bytes, uint8_t* xs,
                                                                 int lanes_log) {
   if (FULL) lanes_log = 5;
   const int64_t i = ((int64_t)blockIdx.x * (32 * kWarps) + threadIdx.x) >> lanes_log;
@@ -508,8 +514,8 @@ __device__ __forceinline__ int entry_row(const int32_t* pos, int64_t i, int64_t 
 // us at 4096 x 10).
 template <int YS, int Y, int V, bool RAGGED, bool FULL, int W, int kSlots>
 __global__ void __launch_bounds__(32 * kWarps, !RAGGED ? 1 : YS == SP24_F32 ? 2 : 3)
-    unsort_kernel(const uint8_t* __restrict__ ys, const int32_t* __restrict__ pos, const float* __restrict__ router_w,
-                  uint32_t units, uint32_t per_row, int topk, int64_t rows, int64_t H, uint8_t* __restrict__ y,
+    unsort_kernel(const uint8_t* ys, const int32_t* pos, const float* router_w,
+                  uint32_t units, uint32_t per_row, int topk, int64_t rows, int64_t H, uint8_t* y,
                   int lanes_log) {
   constexpr int kIn = Elem<YS>::kBytes, kOut = Elem<Y>::kBytes;
   if (FULL) lanes_log = 5;
@@ -598,9 +604,9 @@ template <bool RAGGED>
 constexpr int kPairs = RAGGED ? 2 : 4;
 template <int YS, int Y, int V, bool RAGGED, bool DOT, bool FULL>
 __global__ void __launch_bounds__(32 * kWarps, RAGGED ? 3 : 1) unsort_backward_kernel(
-    const uint8_t* __restrict__ dy, const uint8_t* __restrict__ ys, const int32_t* __restrict__ pos,
-    const float* __restrict__ router_w, int64_t n, int topk, int64_t rows, int64_t H, uint8_t* __restrict__ dys,
-    float* __restrict__ d_router_w, int lanes_log) {
+    const uint8_t* dy, const uint8_t* ys, const int32_t* pos,
+    const float* router_w, int64_t n, int topk, int64_t rows, int64_t H, uint8_t* dys,
+    float* d_router_w, int lanes_log) {
   if (FULL) lanes_log = 5;
   constexpr int kIn = Elem<YS>::kBytes, kOut = Elem<Y>::kBytes;
   const int sub = threadIdx.x & ((1 << lanes_log) - 1);

@@ -48,9 +48,9 @@ __device__ __forceinline__ uint32_t pair_bits(T v) {
 // subtracted from the word at the end.  A scale above 2^100, whose 1 / (15 s) may be subnormal,
 // first has w and itself divided by 2^64.
 template <int DT, int G, bool ZEROS>
-__global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* __restrict__ w, int64_t groups,
-                                                          uint32_t* __restrict__ codes, uint16_t* __restrict__ scales,
-                                                          uint8_t* __restrict__ zeros) {
+__global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* w, int64_t groups,
+                                                          uint32_t* codes, uint16_t* scales,
+                                                          uint8_t* zeros) {
   constexpr int L = G / 16;
   using P = typename Pair16<DT>::T;
   const int lane = threadIdx.x % L;
@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* __restric
     const int64_t at = group * (2 * L) + lane;
     uint4 x[2] = {};
     if (live) {
-      x[0] = ldg_stream16(w + at);
-      x[1] = ldg_stream16(w + at + L);
+      x[0] = load_stream16(w + at);
+      x[1] = load_stream16(w + at + L);
     }
     const uint32_t word[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     float lo = 0.0f, hi = 0.0f;  // symmetric: hi is the largest magnitude
@@ -134,10 +134,10 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const uint4* __restric
 // (exact) times s is one multiplication in that type, which rounds once: [12288, 5120] to bf16 takes 26 us
 // (24 at the copy rate), against 44 with conversions to fp32 and back.
 template <int DT, int ST>
-__global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* __restrict__ codes,
-                                                            const uint16_t* __restrict__ scales,
-                                                            const uint8_t* __restrict__ zeros, int64_t vecs,
-                                                            int span_log, void* __restrict__ out) {
+__global__ void __launch_bounds__(256) dequantize_w4_kernel(const uint32_t* codes,
+                                                            const uint16_t* scales,
+                                                            const uint8_t* zeros, int64_t vecs,
+                                                            int span_log, void* out) {
   constexpr int kTurns = 4;
   begin();
   for (int64_t base = (int64_t)blockIdx.x * (256 * kTurns) + threadIdx.x; base < vecs;

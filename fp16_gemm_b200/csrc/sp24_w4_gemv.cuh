@@ -522,7 +522,7 @@ struct GemvKernel {
         uint4 v[kTok];  // every row's loads in flight together
 #pragma unroll
         for (int m = 0; m < kTok; ++m)
-          if (m < (int)p.M) v[m] = __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)m * pieces + j);
+          if (m < (int)p.M) v[m] = reinterpret_cast<const uint4*>(p.x)[(int64_t)m * pieces + j];
 #pragma unroll
         for (int m = 0; m < kTok; ++m)
           if (m < (int)p.M)
@@ -556,7 +556,7 @@ struct GemvKernel {
 #pragma unroll
           for (int j = 0; j < kAhead; ++j)
             if (kAhead * part + j < blocks)
-              xv[n][j] = __ldg(reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * (kAhead * part + j)));
+              xv[n][j] = *reinterpret_cast<const uint4*>(x_row[n] + 2 * k + 64 * (kAhead * part + j));
     };
     // blocks j, j + 1 of the chunk in the stage
     auto multiply2 = [&](uint32_t stage, int k, int j, const uint4 (&xv)[NT][kAhead], bool both) {

@@ -3,6 +3,8 @@ source, where breaking them would show on a GPU only now and then."""
 import os
 import re
 
+import pytest
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "fp16_gemm_b200", "csrc")
 
 
@@ -19,3 +21,36 @@ def test_waits_of_the_4bit_products_end_for_a_whole_warp():
     waits = re.findall(r"[^;{}]*\bmbar_\w*wait\w*\s*\([^;]*;", code)
     assert len(waits) == 1 and "__all_sync(kFull, tc::mbar_wait(bar, parity))" in waits[0]
     assert len(re.findall(r"\bwarp_wait\(", code)) == 3  # itself, the copying warp, the multiplying warps
+
+
+FILES = [f for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh")) and '#include "sp24_launch.cuh"' in open(os.path.join(CSRC, f)).read()]
+
+
+def _kernels(code):
+    """(parameters, body) of each kernel."""
+    for m in re.finditer(r"__global__\s+void\s+(?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s*)?(\w+)\s*\(", code):
+        ends = []
+        at = m.end() - 1
+        for pair in ("()", "{}"):
+            at = code.index(pair[0], at)
+            depth, start = 0, at
+            while True:
+                depth += (code[at] == pair[0]) - (code[at] == pair[1])
+                at += 1
+                if depth == 0:
+                    break
+            ends.append(code[start + 1:at - 1])
+        yield m.group(1), ends[0], ends[1]
+
+
+def test_files_that_launch_ahead():
+    assert {"sp24_route.cu", "sp24_sort.cu", "sp24_w4.cu", "sp24_w4_gemv.cuh"} <= set(FILES)
+    assert sum(len(list(_kernels(_code(f)))) for f in FILES) >= 11
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_kernels_that_start_early_read_with_ordinary_loads(name):
+    """Their predecessor may still write what they are to read, so no load may take the read-only path,
+    which is defined for data that nobody writes while the kernel runs, and no pointer may tell the
+    compiler that the wait does not concern it."""
+    assert not re.search(r"__ldg\b|ld\.global\.nc|ldg_stream16|__restrict__", _code(name))

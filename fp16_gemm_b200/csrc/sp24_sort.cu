@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(32 * kRankWarps) sort_rank_kernel(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t from = (int64_t)blockIdx.x << t.chunk_log;
   const int mine = (int)min((int64_t)1 << t.chunk_log, t.n - from);
-  bool waited = false;
+  begin();
   for (int e0 = 0; e0 <= t.E; e0 += kCounters) {
     const int span = (int)min((int64_t)kCounters, t.E + 1 - e0);
     for (int e = threadIdx.x; e < span; e += 32 * kRankWarps) held[e] = 0;
@@ -438,9 +438,6 @@ __global__ void __launch_bounds__(32 * kRankWarps) sort_rank_kernel(const __grid
       const bool in = j < mine && key >= 0 && key < span;
       const unsigned same = __match_any_sync(kFull, in ? key : -1);
       const int leader = __ffs(same) - 1;
-      // ids are read ahead of the wait: the kernel before this one, the scan, does not write them
-      if (!waited) begin();
-      waited = true;
       int row = in ? t.first[e0 + key] + t.before[(e0 + key) * t.chunks + blockIdx.x] : 0;
       int base = 0;
       const int warps = min(kRankWarps, (mine - r0 + 31) / 32);

@@ -54,3 +54,24 @@ def test_kernels_that_start_early_read_with_ordinary_loads(name):
     which is defined for data that nobody writes while the kernel runs, and no pointer may tell the
     compiler that the wait does not concern it."""
     assert not re.search(r"__ldg\b|ld\.global\.nc|ldg_stream16|__restrict__", _code(name))
+
+
+@pytest.mark.parametrize("name", [f for f in FILES if f != "sp24_w4_gemv.cuh"])
+def test_kernels_that_start_early_wait_before_they_read(name):
+    """begin() stands once in a kernel, outside of every branch and loop, and no pointer is followed
+    before it."""
+    for kernel, params, body in _kernels(_code(name)):
+        ahead, *rest = body.split("begin();")
+        assert len(rest) == 1, kernel
+        assert ahead.count("{") == ahead.count("}") and ahead.rstrip()[-1:] in ("", ";"), kernel
+        assert not re.search(r"\b(for|while|return)\b", ahead), kernel
+        for p in re.findall(r"\*\s*(?:__restrict__\s+)?(\w+)", params):
+            assert not re.search(rf"\b{p}\s*\[|\*\s*{p}\b", ahead), (kernel, p)
+        assert not re.search(r"\bt\.\w+\s*\[", ahead), kernel
+
+
+def test_the_4bit_products_wait_before_they_read():
+    code = _code("sp24_w4_gemv.cuh")
+    assert code.count("begin();") == 1
+    run = code[code.index("void run("):code.index("begin();")]
+    assert "p." not in run and "return" not in run

@@ -1,6 +1,8 @@
 // The kernel of sp24_gemv_w4 / sp24_gemv_w4_grouped; each type of x is a translation unit of its own.
 #pragma once
 
+#include <atomic>
+
 #include "sp24_launch.cuh"
 #include "sp24_tc.cuh"
 #include "sp24_w4.cuh"
@@ -723,13 +725,13 @@ template <int XT, int NT, int MT, int S, int WK, bool SWIGLU, bool XW, bool ZERO
 int launch_gemv(GemvW4 p, cudaStream_t s) {
   using Kern = GemvKernel<XT, NT, MT, S, WK, SWIGLU, XW, ZEROS, GB>;
   auto kernel = gemv_w4_kernel<XT, NT, MT, S, WK, SWIGLU, XW, ZEROS, GB>;
-  static bool raised[64];  // the attribute holds per device
+  static std::atomic<bool> raised[64];  // the attribute holds per device; threads may set it twice
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SP24_ERR_CUDA;
-  if (!raised[dev]) {
+  if (!raised[dev].load(std::memory_order_relaxed)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
       return SP24_ERR_CUDA;
-    raised[dev] = true;
+    raised[dev].store(true, std::memory_order_relaxed);
   }
   const int64_t cols = SWIGLU ? p.N / 2 : p.N, col_tiles = (cols + Kern::kItemCols - 1) / Kern::kItemCols;
   // with experts: the sum of ceil(rows / kTok) is at most this

@@ -75,3 +75,10 @@ def test_the_4bit_products_wait_before_they_read():
     assert code.count("begin();") == 1
     run = code[code.index("void run("):code.index("begin();")]
     assert "p." not in run and "return" not in run
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_host_state_of_a_launch_is_atomic(name):
+    """What a launch remembers on the host is written by any thread that calls it."""
+    held = [m.group(0) for m in re.finditer(r"\bstatic\s+(?!constexpr|__device__|__host__|_?const\b)[\w:<>]+\s+\w+(\[\w+\])?\s*(=|;|\{)", _code(name))]
+    assert all("std::atomic<" in h for h in held), held

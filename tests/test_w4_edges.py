@@ -93,3 +93,28 @@ def test_offsets_that_name_rows_again_and_again(E, R):
     sp.gemv_w4_grouped(x, w, offsets, out=around[1:-1])
     _cuda_ok()
     assert not around[1:-1].any() and (around[0] == -5).all() and (around[-1] == -5).all()
+
+
+@pytest.mark.gpu
+def test_calls_of_several_threads():
+    """First calls of a form from four host threads at once, each on a stream of its own."""
+    import threading
+    x = torch.randn(3, 1152, generator=_gen(1)).half().cuda()
+    w = random_w4(70, 1152, 64, True, torch.float16, 2)
+    torch.cuda.synchronize()
+    got, start = [None] * 4, threading.Barrier(4)
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        start.wait()
+        got[i] = [sp.gemv_w4(x, w, act, stream=stream) for act in (sp.ACT_NONE, sp.ACT_SWIGLU) for _ in range(8)]
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _cuda_ok()
+    want = [sp.gemv_w4(x, w, act) for act in (sp.ACT_NONE, sp.ACT_SWIGLU) for _ in range(8)]
+    assert all(torch.equal(a, b) for r in got for a, b in zip(r, want))

@@ -212,7 +212,7 @@ int gemv(const void* x, int x_dtype, const sp24_w4_operand* w, const int32_t* of
   if (K && (!x || !w->codes || !w->scales)) return SP24_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w->codes, 16) || !aligned(w->scales, 16) || !aligned(w->zeros, 16)) return SP24_ERR_ALIGN;
   const GemvW4 p{x, w->codes, reinterpret_cast<const uint16_t*>(w->scales), w->zeros, grouped ? offsets : nullptr, y,
-                 M, E, N, K, w->scale_dtype, w->group, y_dtype == SP24_F32, 0, 1};
+                 M, E, N, K, (int16_t)w->scale_dtype, (int16_t)w->group, y_dtype == SP24_F32, 1, 0};
   if (act == SP24_ACT_SWIGLU) return x_dtype == SP24_BF16 ? gemv_w4_swiglu_bf16(p, s) : gemv_w4_swiglu_f16(p, s);
   return x_dtype == SP24_BF16 ? gemv_w4_bf16(p, s) : gemv_w4_f16(p, s);
 }

@@ -19,6 +19,8 @@ struct W4Half<SP24_F16> {
   static __device__ __forceinline__ uint32_t put(float v) { return __half_as_ushort(__float2half_rn(v)); }
 };
 
+// The kernel's parameter block.  Its size shows in a call's time: [5120, 5120] takes 8.3 us a call with 96
+// bytes and 8.8 with 104.
 struct GemvW4 {
   const void* x;
   const uint8_t* codes;
@@ -27,10 +29,11 @@ struct GemvW4 {
   const int32_t* offsets;  // grouped: E + 1
   void* y;
   int64_t M, E, N, K;
-  int scale_dtype, group, y_f32;
+  int16_t scale_dtype, group, y_f32;
+  int16_t share;   // set by the launch: the teams of a CTA that take an item's K together, all or one
   int tile_bound;  // set by the launch, with experts: the most row tiles that ascending offsets give
-  int share;  // set by the launch: the teams of a CTA that take an item's K together, all or one
 };
+static_assert(sizeof(GemvW4) == 96);
 
 int gemv_w4_bf16(const GemvW4& p, cudaStream_t s);
 int gemv_w4_f16(const GemvW4& p, cudaStream_t s);

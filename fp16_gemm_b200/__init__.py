@@ -14,6 +14,9 @@ Routed feed-forward around gemm_grouped / moe_block, and its single-token form w
 
     moe_route -> moe_sort -> gemm_grouped or gemv_w4_grouped -> moe_unsort, each with its _backward
     (moe_sort_backward, moe_unsort_backward, moe_route_backward) where it is differentiable
+
+No entry point records anything for autograd: outputs are detached, also where inputs require
+gradients.  The products (gemm_*, gemv_w4*, moe_block) have no gradient here.
 """
 from __future__ import annotations
 
@@ -996,7 +999,8 @@ def _sort(x, routing, E: int, out, workspace) -> MoeSorted:
 @_placed
 def moe_sort(x: torch.Tensor, routing: torch.Tensor, E: int, out=None, workspace=None) -> MoeSorted:
     """x [T, H] in the order of the experts in routing [T, topk] (stable), with the tables of that
-    order.  An id of -1 is an empty slot; rows of xs behind the last expert's are not written."""
+    order.  An id of -1 is an empty slot; rows of xs behind the last expert's are not written (when
+    allocated here they hold anything)."""
     return _sort(x, routing, E, out, workspace)
 
 
@@ -1039,7 +1043,8 @@ def moe_unsort(ys: torch.Tensor, pos: torch.Tensor, router_w: Optional[torch.Ten
 def moe_unsort_backward(dy: torch.Tensor, ys: torch.Tensor, pos: torch.Tensor, router_w: Optional[torch.Tensor] = None,
                         out=None):
     """(dys, d_router_w) of moe_unsort; rows of dys that no slot names are not written (zeros when
-    allocated here).  Without router_w, d_router_w is None."""
+    allocated here, which takes a fill of the whole of dys first: pass `out` where every row is named
+    or the others do not count).  Without router_w, d_router_w is None."""
     dev = ys.get_device()
     rows, H = _dims(ys, "ys", 2)
     T, topk = _dims(pos, "pos", 2)
@@ -1132,7 +1137,8 @@ def _gemv_out(x, rows: int, N: int, act: int, dtype, out):
 @_placed
 def gemv_w4(x: torch.Tensor, w: W4Tensor, act: int = ACT_NONE, dtype=None, out=None) -> torch.Tensor:
     """y[M, N] = x[M, K] @ value(w)[N, K]^T for a few rows x (f16 / bf16), fp32 (or x's type by
-    `dtype`); ACT_SWIGLU: w holds gate rows then up rows, y[M, N/2] = SiLU(gate) * up in x's type."""
+    `dtype`); ACT_SWIGLU: w holds gate rows then up rows, y[M, N/2] = SiLU(gate) * up in x's type.
+    For many rows: gemm_dense(x, dequantize_w4(w, x.dtype))."""
     dev = x.get_device()
     M, K = _dims(x, "x", 2)
     xp = _arg(x, "x", dev, x.shape, *_HALVES)
@@ -1149,7 +1155,9 @@ def gemv_w4(x: torch.Tensor, w: W4Tensor, act: int = ACT_NONE, dtype=None, out=N
 def gemv_w4_grouped(xs: torch.Tensor, w: W4Tensor, offsets: torch.Tensor, act: int = ACT_NONE, dtype=None,
                     out=None) -> torch.Tensor:
     """gemv_w4 over rows in expert order (moe_sort's xs and offsets [E + 1]) with the E matrices
-    stacked in w; rows from offsets[E] on are not written (zeros when allocated here)."""
+    stacked in w; rows from offsets[E] on are not written (zeros when allocated here, which takes a
+    fill first: pass `out` to save it).  For many rows: gemm_grouped(xs, row_expert[:, None],
+    dequantize_w4(w, xs.dtype), E, N, K)."""
     dev = xs.get_device()
     R, K = _dims(xs, "xs", 2)
     xp = _arg(xs, "xs", dev, xs.shape, *_HALVES)

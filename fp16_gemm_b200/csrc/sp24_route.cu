@@ -12,8 +12,12 @@
 // for rows whose ties leave more than 32, and for E <= 64, where a round is cheap (T = 16384, E = 64,
 // topk = 8: 7.8 against 8.6 us).
 //
-// Bound by instruction issue and the launch: the logits of 4096 tokens over 512 experts are 8.4 MB, 1.3 us at
-// the copy rate; forward 5.5 us, gradient 3.9 us (4.7 where it is dense).
+// The logits of 4096 tokens over 512 experts are 8.4 MB, 1.3 us at the copy rate.  Forward 5.5 us (16-bit
+// logits 5.4), gradient 4.5 us (16-bit 3.9; dense, softmax over all experts, 6.7 for 17 MB); 8 tokens 2.3 and
+// 2.2 us.  A launch and one dependent load are 2.2 us of it.  Not bound by issue (46 % of its
+// slots) nor by HBM (10 %): a token's chain of load, sort of maxima, gather and ranking is latency, with
+// few warps to hide it.  The forward for 512 experts holds 80 registers, so six CTAs fit an SM, and
+// 4096 tokens are 1024 CTAs, 1.15 times what the chip holds at once.
 #include "sp24_launch.cuh"
 
 namespace sp24 {

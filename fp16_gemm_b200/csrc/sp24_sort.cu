@@ -3,9 +3,12 @@
 // sp24.h; [P1] "Concurrency, not sparsity, is the lever" names the routed model).
 //
 // Everything here moves rows; nothing is multiplied more than once, so HBM is the bound.  Measured at
-// 4096 tokens x 10 slots, rows of 2048 bf16 entries (185 MB moved one way, 28 us at the copy rate): sort 36 us
-// (10 of them its tables), its gradient 27 us, unsort 27 us, its gradients 54 us (354 MB, 54 us).  A decode step (8
-// tokens): about 2.5 us each, the time of a launch and two dependent loads.
+// 4096 tokens x 10 slots, rows of 2048 bf16 entries (185 MB moved one way, 28 us at the copy rate): sort 41 us
+// (10.6 of them its tables), its gradient 28 us, unsort 28 us, its gradients 56 us (354 MB, 54 us).  A decode
+// step (8 tokens): 2.4 to 3.9 us each, the time of a launch and two or three dependent loads.
+//
+// Figures are the GPU's time for a call, in a replayed graph of calls on tensors that take turns.  "a
+// against b" is what both forms took side by side when the choice between them was made, a the one that is here.
 #include "sp24_launch.cuh"
 
 namespace sp24 {
@@ -26,8 +29,9 @@ struct Words {
 };
 
 // Rows of tens of thousands of entries pass through L2 once: they are read and written with the
-// evict-first policy (STREAM), which leaves the tokens' own rows (read topk times) there (sort 34
-// against 41 us, unsort 28 against 33, its gradients 57 against 61).
+// evict-first policy (STREAM), which leaves the tokens' own rows (read topk times) there (4096 x 10 rows of
+// [2048]: sort 41 against 42 us, its gradient 28 against 32, unsort 28 against 32; its gradients lose by it,
+// 55.6 against 54.8).
 template <bool STREAM, typename T>
 __device__ __forceinline__ T load_as(const uint8_t* p) {
   return STREAM ? __ldcs(reinterpret_cast<const T*>(p)) : *reinterpret_cast<const T*>(p);
@@ -64,9 +68,9 @@ __device__ __forceinline__ void store_vec(uint8_t* p, const Words<BYTES>& r) {
 // words ("ragged": odd widths, odd bases) are stored with aligned 16-byte vectors all the same, what is
 // ahead of the first and behind the last one by elements.  What a vector is made of is read as the
 // aligned 16-byte pieces around it and shifted, by the same amount all along a row.  4096 x 10 rows of
-// 2047 bf16 entries, against 2-byte accesses: sort 46 and 56 us, unsort 55 and 103, its gradients 84
-// and 110 (what is left are the shifts' instructions; where words do, they are faster: 2046 entries,
-// unsort 34 us).
+// 2047 bf16 entries, against 2-byte accesses: sort 46 against 56 us, unsort 55 against 103, its
+// gradients 84 against 110 (58, 57 and 91 us on tensors that take turns).  What is left are the shifts'
+// instructions; where words do, they are faster (2046 entries: 51, 36 and 77 us).
 template <int BYTES, bool RAGGED>
 struct Window {
   uint32_t w[BYTES / 4 + (RAGGED ? 4 : 0)];
@@ -212,7 +216,7 @@ struct Elem {
 // (one warp per expert) and its last CTA to finish adds up the experts' offsets, the third adds to
 // both the equal entries before entry i in its own chunk, the fourth moves the rows.  At 2000 entries over
 // 512 experts the first way takes 7.0 us and the second 8.2, at 4000 14 and 8.3: the border is at 2048.  The
-// tables take 10 us at 40960 entries and 14 at 163840, most of it launches and dependent loads.
+// tables take 10.6 us at 40960 entries and 13.4 at 163840, most of it launches and dependent loads.
 
 struct SortTables {
   const int32_t* routing;
@@ -285,7 +289,8 @@ __device__ __forceinline__ void copy_ragged(uint8_t* to, const uint8_t* from, in
     reinterpret_cast<uint16_t*>(to)[part.column(e)] =
         e == sub ? edge : reinterpret_cast<const uint16_t*>(from)[part.column(e)];
 }
-// BYTES: 16, 8, 4, or 2 for ragged rows.  FULL: all lanes of a warp (known strides: sort 36 against 37 us).
+// BYTES: 16, 8, 4, or 2 for ragged rows.  FULL: all lanes of a warp (known strides: sort 40.5 against 41.3
+// us, of 16384 x 8 rows of [512] fp32 66 against 71).
 template <int BYTES, bool FULL>
 __device__ __forceinline__ void copy_row(uint8_t* to, const uint8_t* from, int64_t bytes,
                                          const uint8_t* lo, const uint8_t* hi, int lanes_log) {

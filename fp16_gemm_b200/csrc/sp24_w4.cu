@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t pair_bits(T v) {
 // clamp(w / s + z + 2^-16, 0, 15): so it is that of the exact value, and an exact border goes up.
 //
 // Bound by instruction issue before HBM if done plainly (74 us for [12288, 5120] bf16, whose bytes take 24
-// at the copy rate; 26 us as it is, 29 with zero points), so the arithmetic is cut to four
+// at the copy rate; 28 us as it is, 31 with zero points), so the arithmetic is cut to four
 // instructions an entry: unpacking, one saturating fma (the clamp is its saturation), one fma that
 // adds 1.5 * 2^23 (whose last place is 1, which rounds to the integer), and one integer
 // multiply-add that joins the codes with the constant's bits still in them; their sum is

@@ -311,17 +311,25 @@ struct Walk {
 // they come, with x's pairs picked alike.  A group's sum is scaled in fp32.
 //
 // What bounds it: the bytes of codes and scales for large matrices (one token through [151936, 4096],
-// groups of 128: 61 us, 5.2 TB/s, 0.80 of the copy rate; 68 us under sustained load, where the power
-// limit takes the clock from 1965 to 1770 MHz), with instruction issue close behind: a chunk of 16
-// rows, 2 KB, takes about 190 instructions of products proper, and an SM has 88 cycles for it at
-// the copy rate.  Hence warps of their own for the copies (68 against 74 us with every warp copying
+// groups of 128: 62 us, 5.2 TB/s, 0.79 of the copy rate; 72 us under sustained load, where the power
+// limit takes the clock from 1965 to 1732 MHz), with instruction issue behind it: a chunk of 16
+// rows, 2 KB, takes about 190 instructions of products proper, and at the copy rate an SM has 88
+// cycles for it, so 352 issue slots (54 %).  All instructions together fill 65 % of the slots at 0.7 of
+// that rate.  Hence warps of their own for the copies (68 against 74 us with every warp copying
 // for itself: no registers are left for its addresses), chunks of 256 instead of 128 entries, expand8
 // (74 against 80 us with the codes or-ed into 2^7 and a subtraction), and tables copied per stage of
 // four chunks (groups of 32 with zero points: 86 against 146 us with a row's few bytes copied per
-// chunk).  Small matrices are bound by the launch, the first loads and a warp's own latency through
-// its few chunks ([5120, 5120]: 7 us, floor 2.1).  Experts (8 tokens over 10 of 512, SwiGLU,
-// [1024, 2048] each: 25 us, 3.3 TB/s) spend half of their instructions between items of two chunks a
-// warp.
+// chunk; 92 us now, floor 56).  Small matrices are bound by the launch, the first loads and a warp's own
+// latency through its few chunks ([5120, 5120]: 7 us, floor 2.1: its 320 items leave 272 of 592 teams
+// without one).  Experts (8 tokens over 10 of 512, SwiGLU, [1024, 2048] each: 23 us, 3.5 TB/s) spend
+// half of their instructions between items of two chunks a warp.
+//
+// A thread has 96 registers, 640 threads in the CTA.  Kernels with x in shared memory fit or spill at most 28
+// bytes.  Those with x in global memory, experts among them, store 8 to 132 spilled bytes (32 for SwiGLU
+// over experts with groups of 128).
+//
+// Figures are the GPU's time for a call, in a replayed graph of calls on tensors that take turns.  "a
+// against b" is what both forms took side by side when the choice between them was made, a the one that is here.
 //
 // XW: x stands in shared memory whole, its pairs picked when it is brought there; otherwise (experts,
 // or a large x) it is read from global memory half a chunk ahead and its pairs are picked at each use.
@@ -546,8 +554,11 @@ struct GemvKernel {
 
     // x of kAhead blocks of the chunk at entry k, as it stands in memory, read one such part ahead
     constexpr int kAhead = 4, kParts = kChunk / 32 / kAhead;
-    const uint8_t* x_row[NT];  // this lane's rows of x; columns past the last row are 0 (and not stored):
-    int x_on[NT];              // the MMA draws less power so, and power is what limits the clock
+    // This lane's rows of x.  Columns past the last row are not stored.  With x in shared memory they are 0:
+    // the MMA draws less power so, and power is what limits the clock.  Otherwise they repeat the last row
+    // (zeros there, over experts: 25.3 against 24.8 us).
+    const uint8_t* x_row[NT];
+    int x_on[NT];
     // Where the first group of this lane's row of tile i stands within a piece, in bytes; a further stage
     // moves that on unless its groups fill pieces.
     int scale_odd[MT], zero_odd[MT];

@@ -626,9 +626,11 @@ int sp24_dequantize_w4(const sp24_w4_operand* w, int64_t rows, int64_t K, int ou
  *                          projection: y[m, f] = SiLU(v[m, f]) * v[m, N/2 + f], y [M, N/2];
  *                          SiLU(g) = g / (1 + e^-g)
  *   y     device, F32 or x's type (y_dtype)
- * Any number of rows is served, up to sixteen per read of a weight tile: for more than a few dozen
- * rows use the GEMM entry points.  K up to 2^24 and E up to 2^20
- * (SP24_ERR_UNSUPPORTED above).  M == 0,
+ * Any number of rows is served, up to sixteen per read of a weight tile.  The GEMM entry points do
+ * not take this format: for more than a few dozen rows (a prompt) decode the weights once with
+ * sp24_dequantize_w4 to x's type and use sp24_gemm_dense, or over experts (all E matrices decoded)
+ * sp24_gemm_grouped with sp24_moe_sort's xs and row_expert.
+ * K up to 2^24 and E up to 2^20 (SP24_ERR_UNSUPPORTED above).  M == 0,
  * R == 0 or N == 0 is a no-op; K == 0 writes zeros (over experts in their rows only).  One launch, no
  * workspace, no atomics. */
 enum { SP24_ACT_NONE = 0, SP24_ACT_SWIGLU = 1 };

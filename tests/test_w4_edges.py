@@ -1,4 +1,5 @@
-"""Edges of the 4-bit products: waits that run out in every form, experts over no entries."""
+"""Edges of the 4-bit products: waits that run out in every form, experts over no entries, offsets that no sort
+gives, several threads, and the way for many rows."""
 import contextlib
 import ctypes
 
@@ -6,7 +7,7 @@ import pytest
 import torch
 
 import fp16_gemm_b200 as sp
-from test_parity_w4 import _cuda_ok, _gen, random_w4
+from test_parity_w4 import HALF, U, _cuda_ok, _gen, plain_values, random_w4
 
 
 @contextlib.contextmanager
@@ -118,3 +119,28 @@ def test_calls_of_several_threads():
     _cuda_ok()
     want = [sp.gemv_w4(x, w, act) for act in (sp.ACT_NONE, sp.ACT_SWIGLU) for _ in range(8)]
     assert all(torch.equal(a, b) for r in got for a, b in zip(r, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+def test_many_rows_by_decoding_first(dtype):
+    """The documented way for a prompt: decoded weights through the GEMM entry points, one matrix and
+    experts with empty slots.  Each weight is off by half a step of its type; K products are added with
+    at most K + 8 additions, each off by at most two half steps of fp32."""
+    M, N, K, E = 150, 96, 256, 6
+    x = torch.randn(M, K, generator=_gen(1)).to(dtype).cuda()
+    w = random_w4(E * N, K, 64, True, dtype, 2)
+    v, xd = plain_values(w).reshape(E, N, K), x.double().cpu()
+    rel = HALF[dtype] + 2 * (K + 8) * U
+    y = sp.gemm_dense(x, sp.dequantize_w4(sp.W4Tensor(*(t[:N] for t in w)), dtype))
+    assert ((y.double().cpu() - xd @ v[0].t()).abs() <= rel * (xd.abs() @ v[0].abs().t())).all()
+    ids = torch.randint(-1, E, (M, 2), generator=_gen(3)).int()
+    s = sp.moe_sort(x, ids.cuda(), E)
+    rows = sp.gemm_grouped(s.xs, s.row_expert[:, None].contiguous(), sp.dequantize_w4(w, dtype), E, N, K)[:, 0]
+    got = sp.moe_unsort(rows.contiguous(), s.pos)
+    _cuda_ok()
+    held = (ids >= 0).double()[..., None]
+    at = ids.clamp(min=0).long()
+    want = (torch.einsum("tsnk,tk->tsn", v[at], xd) * held).sum(1)
+    mag = (torch.einsum("tsnk,tk->tsn", v[at].abs(), xd.abs()) * held).sum(1)
+    assert ((got.double().cpu() - want).abs() <= (rel + 2 * U) * mag).all()

@@ -97,3 +97,26 @@ def test_grouped_slots_without_an_expert_are_zero(form):
     torch.cuda.synchronize()
     assert sp.last_device_error() == sp.OK
     assert torch.isfinite(rows).all() and not rows[int(s.offsets[-1]):].any()
+
+
+@pytest.mark.parametrize("N,off", [(128, 0), (256, 1), (384, 2), (128, 4)])
+def test_grouped_zeros_stay_in_their_rows(N, off):
+    """The tensor-core path into a y that starts off 16 bytes: slots without an expert first, last, alone
+    and side by side; nothing beside y is written."""
+    E, K, T, topk = 3, 256, 333, 3
+    g = torch.Generator().manual_seed(N)
+    x = torch.randn(T, K, generator=g).bfloat16().cuda()
+    w = sp.quantize_nvfp4((torch.randn(E * N, K, generator=g) * 0.05).bfloat16().cuda())
+    routing = torch.randint(0, E, (T, topk), generator=g).int()
+    empty = torch.rand(T, topk, generator=g) < 0.2
+    empty[0, 0] = empty[-1, -1] = True
+    empty[50:80] = True
+    routing, empty = routing.cuda(), empty.cuda()
+    flat = torch.full((T * topk * N + off + 8,), 7.0, device="cuda")
+    y = flat[off:off + T * topk * N].view(T, topk, N)
+    sp.gemm_grouped(x, routing.masked_fill(empty, -1), w, E, N, K, out=y)
+    torch.cuda.synchronize()
+    assert sp.last_device_error() == sp.OK
+    want = sp.gemm_grouped(x, routing, w, E, N, K).masked_fill(empty[..., None], 0.0)
+    assert torch.equal(y, want)
+    assert (flat[:off] == 7.0).all() and (flat[off + T * topk * N:] == 7.0).all()
